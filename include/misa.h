@@ -6,7 +6,8 @@
  * block pooling of indexer keys (Eq. 4), the block-pooled head router
  * (Eqs. 7-8), routed token scoring with top-k selection (Eqs. 9-10), the dense
  * DSA indexer the method replaces (Introduction, Eqs. 1-2), and the
- * hierarchical MISA-dagger re-rank (Eqs. 11-12).
+ * hierarchical MISA-dagger re-rank (Eqs. 11-12); and what uses their selection: attention
+ * over a paged key-value cache, with the upkeep of that cache ("Paged key-value cache" below).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -64,6 +65,7 @@ extern "C" {
 #define MISA_ERR_BAD_DEVICE_INPUT    6  /* device data out of range (pos >= L, cand)     */
 #define MISA_ERR_STATIC_SCRATCH_TOO_SMALL 7  /* call larger than the fixed scratch of
                                                 misa_score_topk_noalloc                 */
+#define MISA_ERR_OUT_OF_PAGES        8  /* misa_pages_resize: not enough free pages      */
 
 /* Operation ids for misa_workspace_size. */
 #define MISA_OP_ROUTE_HEADS   1
@@ -78,6 +80,11 @@ extern "C" {
 #define MISA_MAX_HEADS       128
 #define MISA_MAX_ROUTED      128  /* h <= H <= MISA_MAX_HEADS */
 #define MISA_MAX_TOPK        16384
+#define MISA_MAX_POOLS       256  /* pools of one misa_pages_* call */
+
+/* Element types of the paged cache. */
+#define MISA_DTYPE_BF16 0
+#define MISA_DTYPE_FP16 1
 
 /*
  * Bytes of workspace the operation `op` needs for these sizes (0 on invalid
@@ -217,12 +224,120 @@ int misa_score_topk_noalloc(const uint16_t* q, const float* w, const uint16_t* k
                             int d, int64_t L, int h, int topk, int32_t* idx, float* vals,
                             int32_t* device_status, void* stream);
 
+/*
+ * Paged key-value cache
+ * ---------------------
+ * A pool holds num_pages pages of page_size tokens; sequence n keeps its tokens
+ * i * page_size .. (i + 1) * page_size - 1 in page page_table[n, i].
+ *     k_cache, v_cache  16-bit [num_pages, page_size, Hkv, d]  (MISA_DTYPE_*; d = 64 or 128)
+ *     page_table        int32  [nseq, max_pages], -1: no page
+ *     refs              int32  [num_pages], the table entries that name the page; 0: free
+ * Any page_size from 1 on; max_pages * page_size <= 2^30, num_pages <= 2^30,
+ * num_pages * page_size < 2^31.  Tensors whose rows are moved (q, k_new, v_new, out, caches,
+ * pools) are 16-byte aligned.
+ * Scratch and status differ from the calls above in one way, so that calls on different
+ * streams and captured graphs share nothing: `ws` is scratch only (256-byte aligned, any
+ * contents, not used by two calls that overlap on the GPU), and conditions that only the GPU can
+ * see go to device_status (nullable; int32 on the device, zeroed once by the caller, the first
+ * condition wins and stays until misa_check_device_status(device_status, stream)).
+ */
+
+/*
+ * Attention of new tokens over a paged cache: for query row (n, t) and head j,
+ *   z[s] = scale * (q[n, t, j] . k[s, j / (Hq / Hkv)]),  p = softmax of z over the tokens seen,
+ *   out[n, t, j] = sum_s p[s] v[s, j / (Hq / Hkv)],      lse[n, t, j] = ln sum_s exp z[s].
+ * Tokens seen: idx NULL (topk 0): the prefix s = 0 .. pos[n, t].  Otherwise the tokens
+ * idx[n, t, 0 .. topk) (as written by misa_score_topk, dsa_score_topk, misa_dagger_rerank and
+ * hisa_block_filter_topk): any order, -1 = empty slot, each in [0, pos]; a token that is listed
+ * twice counts twice.  Hq must be a multiple of Hkv.
+ * pos = -1 marks a padded row, which sees nothing.  A row that sees nothing (or only scores of
+ * -inf) gets out 0 and lse -inf; cache rows that no query sees are not read, so they may hold
+ * anything.  Reported and skipped: idx entries outside their query's prefix, tokens whose page
+ * entry is not in [0, num_pages).  Reported and clamped: pos outside [-1, max_pages *
+ * page_size).  q, out: dtype, [nseq, T, Hq, d]; lse (nullable) fp32 [nseq, T, Hq].  Sums and
+ * softmax statistics are fp32; the weights p are rounded to dtype for their product with v.
+ * Made for few queries per sequence (decode, drafts): queries beyond 32 / (Hq / Hkv) read the
+ * cache again.  ws: misa_paged_attention_workspace_size(...) bytes.
+ */
+size_t misa_paged_attention_workspace_size(int nseq, int T, int Hq, int Hkv, int d, int topk);
+int misa_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* page_table, const int32_t* pos, const int32_t* idx,
+                         int dtype, int nseq, int T, int Hq, int Hkv, int d, int num_pages,
+                         int page_size, int max_pages, int topk, float scale, void* out,
+                         float* lse, int32_t* device_status, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * The keys and values of new tokens into their pages: row (n, t) of k_new / v_new (dtype,
+ * [nseq, T, Hkv, d]) becomes token pos[n, t] of sequence n; pos = -1 skips the row (padding).
+ * Everything else in the caches stays.  The rows of a call must name different cache rows
+ * (with two for one, which of them each 16 bytes come from is undefined), and a page that others
+ * hold too is theirs as well: misa_pages_resize copies it first.  Reported and skipped: pos
+ * outside [-1, max_pages * page_size), page entries outside [0, num_pages).  No workspace.
+ */
+int misa_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
+                      const int32_t* page_table, int dtype, int nseq, int T, int Hkv, int d,
+                      int num_pages, int page_size, int max_pages, void* k_cache, void* v_cache,
+                      int32_t* device_status, void* stream);
+
+/*
+ * Upkeep of the pages.  Each call reads page_table and refs and writes out_table and out_refs,
+ * which may be the same buffers (in place) but must not overlap them otherwise.  `pools` (a host
+ * array of npools device pointers; NULL with npools 0) lists every pool that the table pages,
+ * e.g. the k_cache and v_cache of all layers: pool i is [num_pages, page_bytes[i]], page_bytes[i]
+ * a multiple of 16.  Pools must not overlap one another.  ws: misa_pages_workspace_size(...)
+ * bytes.
+ */
+size_t misa_pages_workspace_size(int nseq, int max_pages, int num_pages);
+
+/*
+ * Gives every sequence the pages for new_len[n] tokens, where it held those for old_len[n]
+ * (int32 [nseq], 0 .. max_pages * page_size; entries from ceil(old_len / page_size) on count as
+ * empty).  new_len 0 ends a sequence.
+ *   - Growing: slots ceil(old / page_size) .. ceil(new / page_size) - 1 take free pages.  A
+ *     partly filled last page that others hold too (refs > 1) is replaced by a copy of its
+ *     contents in every pool, so that the new tokens may be written; where all its holders grow
+ *     in this call, the one with the highest n keeps the page itself.
+ *   - Shrinking: the slots from ceil(new / page_size) on become -1 and let go of their pages.
+ * Pages are taken lowest first, in the order (sequence, slot), from those that are free before
+ * the call; pages let go of are free after it.  When too few are free, MISA_ERR_OUT_OF_PAGES is
+ * reported and nothing changes.  Reported, the row stays as it is: lengths out of range.
+ */
+int misa_pages_resize(const int32_t* page_table, const int32_t* refs, const int32_t* old_len,
+                      const int32_t* new_len, int nseq, int max_pages, int num_pages,
+                      int page_size, void* const* pools, const int64_t* page_bytes, int npools,
+                      int32_t* out_table, int32_t* out_refs, int32_t* device_status, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * Row n takes the pages of row parent[n] as they were before the call (int32 [nseq]; n: the row
+ * stays, -1: it holds nothing afterwards), all rows at once, as a beam search reorders its
+ * beams.  No page is copied: refs counts the holders.  Reported, the row stays: a parent outside
+ * [-1, nseq).
+ */
+int misa_pages_fork(const int32_t* page_table, const int32_t* refs, const int32_t* parent,
+                    int nseq, int max_pages, int num_pages, int32_t* out_table,
+                    int32_t* out_refs, int32_t* device_status, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/*
+ * Moves the pages in use to the front of the pools: with n_live pages in use, the i-th lowest
+ * of those at or above n_live moves into the i-th lowest free page below it (contents of every
+ * pool, table entries and counts).  n_live (nullable) receives n_live on the device; the pages
+ * from there on are free afterwards.  Reported, left as they are: table entries outside
+ * [-1, num_pages), or naming a page at or above n_live that refs says is free.
+ */
+int misa_pages_compact(const int32_t* page_table, const int32_t* refs, int nseq, int max_pages,
+                       int num_pages, void* const* pools, const int64_t* page_bytes, int npools,
+                       int32_t* out_table, int32_t* out_refs, int32_t* n_live,
+                       int32_t* device_status, void* ws, size_t ws_bytes, void* stream);
+
 /* Static text for a status code.  Host-only. */
 const char* misa_status_string(int status);
 
 /*
- * Synchronise `stream`, read the workspace status word, clear it, and return it
- * (MISA_OK when no device-side condition was recorded).
+ * Synchronise `stream`, read the workspace status word (or a device_status word), clear it,
+ * and return it (MISA_OK when no device-side condition was recorded).
  */
 int misa_check_device_status(void* ws, void* stream);
 

@@ -21,6 +21,11 @@ from ._binding import (  # noqa: F401
     library,
     misa_check_device_status,
     misa_dagger_rerank,
+    misa_paged_append,
+    misa_paged_attention,
+    misa_pages_compact,
+    misa_pages_fork,
+    misa_pages_resize,
     misa_pool_keys,
     misa_pool_keys_range,
     misa_route_heads,

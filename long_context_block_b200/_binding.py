@@ -51,6 +51,16 @@ _SIGS = {
     "hisa_block_filter_topk": (_c_int, [_p, _p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int,
                                         _c_i64, _c_int, _c_int, _c_int, _p, _p, _p, _p, _c_sz,
                                         _p]),
+    "misa_paged_attention_workspace_size": (_c_sz, [_c_int] * 6),
+    "misa_paged_attention": (_c_int, [_p] * 6 + [_c_int] * 10 + [ctypes.c_float] + [_p] * 4
+                             + [_c_sz, _p]),
+    "misa_paged_append": (_c_int, [_p] * 4 + [_c_int] * 8 + [_p] * 4),
+    "misa_pages_workspace_size": (_c_sz, [_c_int] * 3),
+    "misa_pages_resize": (_c_int, [_p] * 4 + [_c_int] * 4 + [_p, _p, _c_int] + [_p] * 4
+                          + [_c_sz, _p]),
+    "misa_pages_fork": (_c_int, [_p] * 3 + [_c_int] * 3 + [_p] * 4 + [_c_sz, _p]),
+    "misa_pages_compact": (_c_int, [_p] * 2 + [_c_int] * 3 + [_p, _p, _c_int] + [_p] * 5
+                           + [_c_sz, _p]),
     "misa_testing_score_simt": (_c_int, [_p, _p, _p, _p, _p, _p, _p, _c_int, _c_int, _c_int,
                                          _c_int, _c_i64, _c_int, _c_i64, _p, _p, _c_sz, _p]),
     "misa_testing_score_rows_wait_expiry": (_c_int, [_p, _p, _p, _p, _p, _c_int, _c_int, _c_int,
@@ -154,12 +164,44 @@ def misa_workspace_size(op, nseq, T, H, d, L, B, h, topk, kprime) -> int:
     return int(_lib.misa_workspace_size(op, nseq, T, H, d, L, B, h, topk, kprime))
 
 
+class _Status:
+    """The device status word of the paged-cache calls, one per device, kept for good: captured
+    graphs hold its address.  The calls only ever write to it atomically, so streams share it."""
+
+    def __init__(self):
+        self._word = {}
+        self._lock = threading.Lock()
+
+    def get(self, device: torch.device) -> torch.Tensor:
+        w = self._word.get(device.index)
+        if w is None:
+            with self._lock:
+                w = self._word.get(device.index)
+                if w is None:
+                    if torch.cuda.is_current_stream_capturing():
+                        raise RuntimeError("the first paged-cache call on a device allocates its "
+                                           "status word: make one before capturing a graph")
+                    w = torch.zeros(64, dtype=torch.int32, device=device)
+                    torch.cuda.current_stream(device).synchronize()   # zero for every stream
+                    self._word[device.index] = w
+        return w
+
+    def find(self, index: int) -> torch.Tensor | None:
+        return self._word.get(index)
+
+
+_STATUS = _Status()
+
+
 def misa_check_device_status(device=None) -> int:
-    """Synchronise, read and clear the workspace status word; raise if it is set."""
+    """Synchronise the current stream, read and clear the status words (the workspace's and the
+    paged-cache calls'); raise if one is set."""
     dev = torch.device(device if device is not None else torch.cuda.current_device())
     ws = _WS.get(256, dev)
     st = int(_lib.misa_check_device_status(_ptr(ws), _stream()))
-    _check("misa_check_device_status", st)
+    word = _STATUS.find(dev.index if dev.index is not None else torch.cuda.current_device())
+    paged = int(_lib.misa_check_device_status(_ptr(word), _stream())) if word is not None else 0
+    _check("misa_check_device_status", st or paged)
     return st
 
 
@@ -364,6 +406,191 @@ def misa_score_topk_noalloc(q, w, k, heads, pos, topk: int, return_vals: bool = 
                                         T, H, d, L, h, topk, _ptr(idx), _ptr(vals),
                                         _ptr(device_status), _stream()))
     return (idx, vals) if return_vals else idx
+
+
+# ----------------------------------------------------------------- paged key-value cache
+# Scratch is a fresh tensor of torch's caching allocator per call: it belongs to the call's
+# stream, and under graph capture to the graph, so neither streams nor graphs share it.
+
+_CACHE_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _scratch(nbytes: int, device) -> torch.Tensor:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _shape(t: torch.Tensor, shape: tuple, name: str):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _cache(k_cache, v_cache, page_table, pos):
+    """Checks what attention and append share; returns the dtype code and the cache's sizes."""
+    if k_cache.dtype not in _CACHE_DTYPES:
+        raise TypeError(f"k_cache must be bf16 or fp16, got {k_cache.dtype}")
+    _dev(k_cache, "k_cache")
+    _dev(v_cache, "v_cache", k_cache.dtype)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, page_size, Hkv, d]")
+    _shape(v_cache, tuple(k_cache.shape), "v_cache")
+    _dev(page_table, "page_table", torch.int32)
+    _dev(pos, "pos", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [nseq, max_pages]")
+    return _CACHE_DTYPES[k_cache.dtype], k_cache.shape
+
+
+def misa_paged_attention(q, k_cache, v_cache, page_table, pos, idx=None,
+                         scale: float | None = None, return_lse: bool = False, out=None,
+                         lse=None):
+    """Attention of new tokens over a paged cache: each query's prefix 0 .. pos, or the tokens
+    of its idx row (an indexer's selection, -1 padded).
+
+    q [nseq, T, Hq, d], k_cache / v_cache [num_pages, page_size, Hkv, d] (bf16 or fp16, one type),
+    page_table int32 [nseq, max_pages], pos int32 [nseq, T] (-1: a padded row), idx int32
+    [nseq, T, topk]; scale defaults to d ** -0.5.  Returns out [nseq, T, Hq, d], and with
+    return_lse also lse fp32 [nseq, T, Hq]."""
+    code, (num_pages, page_size, Hkv, d) = _cache(k_cache, v_cache, page_table, pos)
+    _dev(q, "q", k_cache.dtype)
+    if q.dim() != 4:
+        raise ValueError("q must be [nseq, T, Hq, d]")
+    nseq, T, Hq, _ = q.shape
+    _shape(q, (nseq, T, Hq, d), "q")
+    _shape(pos, (nseq, T), "pos")
+    if page_table.shape[0] != nseq:
+        raise ValueError(f"page_table must have {nseq} rows, got {page_table.shape[0]}")
+    topk = 0
+    if idx is not None:
+        _dev(idx, "idx", torch.int32)
+        topk = idx.shape[-1]
+        _shape(idx, (nseq, T, topk), "idx")
+        if topk == 0:
+            raise ValueError("idx must list at least one token")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _dev(out, "out", q.dtype)
+        _shape(out, tuple(q.shape), "out")
+    if lse is not None:
+        _dev(lse, "lse", torch.float32)
+        _shape(lse, (nseq, T, Hq), "lse")
+    elif return_lse:
+        lse = torch.empty((nseq, T, Hq), dtype=torch.float32, device=q.device)
+    nb = int(_lib.misa_paged_attention_workspace_size(nseq, T, Hq, Hkv, d, topk))
+    ws = _scratch(nb, q.device) if nb else None
+    _check("misa_paged_attention",
+           _lib.misa_paged_attention(
+               q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+               pos.data_ptr(), _ptr(idx), code, nseq, T, Hq, Hkv, d, num_pages, page_size,
+               page_table.shape[1], topk, d ** -0.5 if scale is None else scale, out.data_ptr(),
+               _ptr(lse), _STATUS.get(q.device).data_ptr(), _ptr(ws), nb, _stream()))
+    return (out, lse) if return_lse else out
+
+
+def misa_paged_append(k_new, v_new, pos, page_table, k_cache, v_cache):
+    """Write the keys and values of new tokens ([nseq, T, Hkv, d]) into their pages: row (n, t)
+    becomes token pos[n, t] of sequence n (-1: skipped).  In place; returns the caches."""
+    code, (num_pages, page_size, Hkv, d) = _cache(k_cache, v_cache, page_table, pos)
+    _dev(k_new, "k_new", k_cache.dtype)
+    _dev(v_new, "v_new", k_cache.dtype)
+    nseq, T = pos.shape
+    _shape(k_new, (nseq, T, Hkv, d), "k_new")
+    _shape(v_new, (nseq, T, Hkv, d), "v_new")
+    if page_table.shape[0] != nseq:
+        raise ValueError(f"page_table must have {nseq} rows, got {page_table.shape[0]}")
+    _check("misa_paged_append",
+           _lib.misa_paged_append(
+               k_new.data_ptr(), v_new.data_ptr(), pos.data_ptr(), page_table.data_ptr(), code,
+               nseq, T, Hkv, d, num_pages, page_size, page_table.shape[1], k_cache.data_ptr(),
+               v_cache.data_ptr(), _STATUS.get(k_cache.device).data_ptr(), _stream()))
+    return k_cache, v_cache
+
+
+def _upkeep(page_table, refs, out_table, out_refs):
+    _dev(page_table, "page_table", torch.int32)
+    _dev(refs, "refs", torch.int32)
+    if page_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("page_table must be [nseq, max_pages] and refs [num_pages]")
+    if out_table is None:
+        out_table = torch.empty_like(page_table)
+    else:
+        _dev(out_table, "out_table", torch.int32)
+        _shape(out_table, tuple(page_table.shape), "out_table")
+    if out_refs is None:
+        out_refs = torch.empty_like(refs)
+    else:
+        _dev(out_refs, "out_refs", torch.int32)
+        _shape(out_refs, tuple(refs.shape), "out_refs")
+    nb = int(_lib.misa_pages_workspace_size(*page_table.shape, refs.shape[0]))
+    return out_table, out_refs, _scratch(nb, refs.device) if nb else None, nb
+
+
+def _pools(pools, num_pages: int):
+    n = len(pools)
+    if n == 0:
+        return None, None, 0
+    for i, t in enumerate(pools):
+        _dev(t, f"pools[{i}]")
+        if t.dim() < 1 or t.shape[0] != num_pages:
+            raise ValueError(f"pools[{i}] must have {num_pages} pages")
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in pools])
+    sizes = (ctypes.c_int64 * n)(*[t.numel() // num_pages * t.element_size() for t in pools])
+    return ptrs, sizes, n
+
+
+def misa_pages_resize(page_table, refs, old_len, new_len, page_size: int, pools=(),
+                      out_table=None, out_refs=None):
+    """Give every sequence the pages for new_len tokens where it held those for old_len: take
+    free pages (lowest first), copy a shared, partly filled last page in every pool before it is
+    written, let go of pages.  Returns (page_table, refs); pass out_table=page_table,
+    out_refs=refs for in place.  With too few free pages nothing changes, and
+    misa_check_device_status reports it."""
+    out_table, out_refs, ws, nb = _upkeep(page_table, refs, out_table, out_refs)
+    nseq, max_pages = page_table.shape
+    for t, name in ((old_len, "old_len"), (new_len, "new_len")):
+        _dev(t, name, torch.int32)
+        _shape(t, (nseq,), name)
+    ptrs, sizes, n = _pools(pools, refs.shape[0])
+    _check("misa_pages_resize",
+           _lib.misa_pages_resize(
+               page_table.data_ptr(), refs.data_ptr(), old_len.data_ptr(), new_len.data_ptr(),
+               nseq, max_pages, refs.shape[0], page_size, ptrs, sizes, n, out_table.data_ptr(),
+               out_refs.data_ptr(), _STATUS.get(refs.device).data_ptr(), _ptr(ws), nb, _stream()))
+    return out_table, out_refs
+
+
+def misa_pages_fork(page_table, refs, parent, out_table=None, out_refs=None):
+    """Row n takes the pages of row parent[n] (-1: none), all rows at once; refs follow and no
+    page is copied.  Returns (page_table, refs)."""
+    out_table, out_refs, ws, nb = _upkeep(page_table, refs, out_table, out_refs)
+    nseq, max_pages = page_table.shape
+    _dev(parent, "parent", torch.int32)
+    _shape(parent, (nseq,), "parent")
+    _check("misa_pages_fork",
+           _lib.misa_pages_fork(
+               page_table.data_ptr(), refs.data_ptr(), parent.data_ptr(), nseq, max_pages,
+               refs.shape[0], out_table.data_ptr(), out_refs.data_ptr(),
+               _STATUS.get(refs.device).data_ptr(), _ptr(ws), nb, _stream()))
+    return out_table, out_refs
+
+
+def misa_pages_compact(page_table, refs, pools=(), out_table=None, out_refs=None, n_live=None):
+    """Move the pages in use to the front of the pools (contents, table and counts).  Returns
+    (page_table, refs, n_live): n_live int32 [1], the pages in use."""
+    out_table, out_refs, ws, nb = _upkeep(page_table, refs, out_table, out_refs)
+    nseq, max_pages = page_table.shape
+    if n_live is None:
+        n_live = torch.empty(1, dtype=torch.int32, device=refs.device)
+    else:
+        _dev(n_live, "n_live", torch.int32)
+        _shape(n_live, (1,), "n_live")
+    ptrs, sizes, n = _pools(pools, refs.shape[0])
+    _check("misa_pages_compact",
+           _lib.misa_pages_compact(
+               page_table.data_ptr(), refs.data_ptr(), nseq, max_pages, refs.shape[0], ptrs,
+               sizes, n, out_table.data_ptr(), out_refs.data_ptr(), n_live.data_ptr(),
+               _STATUS.get(refs.device).data_ptr(), _ptr(ws), nb, _stream()))
+    return out_table, out_refs, n_live
 
 
 # ----------------------------------------------------------------- test-only entry points

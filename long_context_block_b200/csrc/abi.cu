@@ -317,6 +317,7 @@ const char* misa_status_string(int status) {
     case MISA_ERR_BAD_DEVICE_INPUT: return "device input out of range (pos, head id or candidate)";
     case MISA_ERR_STATIC_SCRATCH_TOO_SMALL:
       return "call exceeds the fixed scratch of misa_score_topk_noalloc (nseq*T*L > 4194304)";
+    case MISA_ERR_OUT_OF_PAGES: return "not enough free pages";
     default: return "unknown status";
   }
 }

@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "misa.h"
+
 namespace misa {
 
 // Launch with programmatic dependent launch allowed: the kernel may be scheduled while the
@@ -172,5 +174,48 @@ int topk_sort_size(int topk);
 cudaError_t launch_sort_candidates(const int32_t* cand, const int32_t* pos, int rows,
                                    int64_t L, int kprime, int32_t* sorted, int32_t* count,
                                    int* status, cudaStream_t st);
+
+// K9 -- attention of new tokens over a paged cache (paged_attn.cu): the prefix form (topk 0) or
+// the tokens of idx.  scratch: paged_attn_ws_bytes(p) bytes, 256-aligned, any contents.
+struct PagedAttn {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* page_table;
+  const int32_t* pos;
+  const int32_t* idx;
+  void* out;
+  float* lse;
+  int dtype, nseq, T, Hq, Hkv, d, num_pages, page_size, max_pages, topk;
+  float scale;
+};
+size_t paged_attn_ws_bytes(const PagedAttn& p);
+cudaError_t launch_paged_attn(const PagedAttn& p, void* scratch, int* status, cudaStream_t st);
+
+// K10 -- new keys and values into their pages (paged_append.cu).  row_bytes: Hkv * d * 2.
+cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
+                                const int32_t* page_table, int nseq, int T, int row_bytes,
+                                int num_pages, int page_size, int max_pages, void* k_cache,
+                                void* v_cache, int* status, cudaStream_t st);
+
+// K11 -- upkeep of the pages (pages.cu).
+//   PagePools: the pools whose page contents follow a moved or copied page (a kernel argument).
+struct PagePools {
+  int n;
+  unsigned char* base[MISA_MAX_POOLS];
+  uint32_t page_bytes[MISA_MAX_POOLS];   // multiples of 16
+};
+size_t pages_ws_bytes(int nseq, int num_pages);
+cudaError_t launch_pages_resize(const int32_t* table, const int32_t* refs, const int32_t* old_len,
+                                const int32_t* new_len, int nseq, int max_pages, int num_pages,
+                                int page_size, const PagePools& pools, int32_t* out_table,
+                                int32_t* out_refs, void* scratch, int* status, cudaStream_t st);
+cudaError_t launch_pages_fork(const int32_t* table, const int32_t* refs, const int32_t* parent,
+                              int nseq, int max_pages, int num_pages, int32_t* out_table,
+                              int32_t* out_refs, void* scratch, int* status, cudaStream_t st);
+cudaError_t launch_pages_compact(const int32_t* table, const int32_t* refs, int nseq,
+                                 int max_pages, int num_pages, const PagePools& pools,
+                                 int32_t* out_table, int32_t* out_refs, int32_t* n_live,
+                                 void* scratch, int* status, cudaStream_t st);
 
 }  // namespace misa
