@@ -74,6 +74,10 @@ extern "C" {
 #define MISA_OP_DAGGER_RERANK 4
 #define MISA_OP_SCORE_ROWS    5
 #define MISA_OP_HISA_TOPK     6
+/* Operation ids for misa_pages_workspace_size. */
+#define MISA_OP_PAGES_RESIZE  7
+#define MISA_OP_PAGES_FORK    8
+#define MISA_OP_PAGES_COMPACT 9
 
 /* Limits of this build (larger values return MISA_ERR_UNSUPPORTED). */
 #define MISA_HEAD_DIM        128
@@ -232,7 +236,7 @@ int misa_score_topk_noalloc(const uint16_t* q, const float* w, const uint16_t* k
  *     k_cache, v_cache  16-bit [num_pages, page_size, Hkv, d]  (MISA_DTYPE_*; d = 64 or 128)
  *     page_table        int32  [nseq, max_pages], -1: no page
  *     refs              int32  [num_pages], the table entries that name the page; 0: free
- * Any page_size from 1 on; max_pages * page_size <= 2^30, num_pages <= 2^30,
+ * Any page_size from 1 on; max_pages * page_size, nseq * max_pages and num_pages <= 2^30,
  * num_pages * page_size < 2^31.  Tensors whose rows are moved (q, k_new, v_new, out, caches,
  * pools) are 16-byte aligned.
  * Scratch and status differ from the calls above in one way, so that calls on different
@@ -257,9 +261,11 @@ int misa_score_topk_noalloc(const uint16_t* q, const float* w, const uint16_t* k
  * page_size).  q, out: dtype, [nseq, T, Hq, d]; lse (nullable) fp32 [nseq, T, Hq].  Sums and
  * softmax statistics are fp32; the weights p are rounded to dtype for their product with v.
  * Made for few queries per sequence (decode, drafts): queries beyond 32 / (Hq / Hkv) read the
- * cache again.  ws: misa_paged_attention_workspace_size(...) bytes.
+ * cache again.  ws: misa_paged_attention_workspace_size(...) bytes (0 where few or short items
+ * need none, and on invalid arguments; ws may then be NULL).
  */
-size_t misa_paged_attention_workspace_size(int nseq, int T, int Hq, int Hkv, int d, int topk);
+size_t misa_paged_attention_workspace_size(int nseq, int T, int Hq, int Hkv, int d,
+                                           int page_size, int max_pages, int topk);
 int misa_paged_attention(const void* q, const void* k_cache, const void* v_cache,
                          const int32_t* page_table, const int32_t* pos, const int32_t* idx,
                          int dtype, int nseq, int T, int Hq, int Hkv, int d, int num_pages,
@@ -285,10 +291,10 @@ int misa_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
  * which may be the same buffers (in place) but must not overlap them otherwise.  `pools` (a host
  * array of npools device pointers; NULL with npools 0) lists every pool that the table pages,
  * e.g. the k_cache and v_cache of all layers: pool i is [num_pages, page_bytes[i]], page_bytes[i]
- * a multiple of 16.  Pools must not overlap one another.  ws: misa_pages_workspace_size(...)
- * bytes.
+ * a multiple of 16.  Pools must not overlap one another.  ws: misa_pages_workspace_size(op,
+ * ...) bytes (0, and ws may be NULL, where none is needed; 0 on invalid arguments too).
  */
-size_t misa_pages_workspace_size(int nseq, int max_pages, int num_pages);
+size_t misa_pages_workspace_size(int op, int nseq, int max_pages, int num_pages);
 
 /*
  * Gives every sequence the pages for new_len[n] tokens, where it held those for old_len[n]

@@ -25,7 +25,7 @@ constexpr int64_t kMaxSpan = int64_t(1) << 30;
 
 int check_table(int nseq, int max_pages, int num_pages) {
   if (nseq < 1 || max_pages < 1 || num_pages < 1) return MISA_ERR_INVALID_ARG;
-  if (num_pages > kMaxSpan) return MISA_ERR_UNSUPPORTED;
+  if (num_pages > kMaxSpan || (int64_t)nseq * max_pages > kMaxSpan) return MISA_ERR_UNSUPPORTED;
   return MISA_OK;
 }
 
@@ -49,6 +49,7 @@ int check_heads(int nseq, int T, int Hq, int Hkv, int topk) {
 }
 
 int check_scratch(void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return MISA_OK;
   if (ws_bytes < need) return MISA_ERR_WORKSPACE_TOO_SMALL;
   return check_dev(ws, need, 256);
 }
@@ -60,7 +61,7 @@ int check_out(const void* in, const void* out, size_t bytes) {
   return a < b + bytes && b < a + bytes ? MISA_ERR_INVALID_ARG : MISA_OK;
 }
 
-int check_upkeep(const int32_t* table, const int32_t* refs, int nseq, int max_pages,
+int check_upkeep(int op, const int32_t* table, const int32_t* refs, int nseq, int max_pages,
                  int num_pages, const int32_t* out_table, const int32_t* out_refs, void* ws,
                  size_t ws_bytes) {
   const size_t tb = (size_t)nseq * max_pages * 4, rb = (size_t)num_pages * 4;
@@ -70,7 +71,7 @@ int check_upkeep(const int32_t* table, const int32_t* refs, int nseq, int max_pa
   MISA_TRY(check_dev(out_refs, rb, 4));
   MISA_TRY(check_out(table, out_table, tb));
   MISA_TRY(check_out(refs, out_refs, rb));
-  return check_scratch(ws, ws_bytes, misa_pages_workspace_size(nseq, max_pages, num_pages));
+  return check_scratch(ws, ws_bytes, misa_pages_workspace_size(op, nseq, max_pages, num_pages));
 }
 
 int take_pools(void* const* pools, const int64_t* page_bytes, int npools, int num_pages,
@@ -93,8 +94,9 @@ int take_pools(void* const* pools, const int64_t* page_bytes, int npools, int nu
 
 extern "C" {
 
-size_t misa_paged_attention_workspace_size(int nseq, int T, int Hq, int Hkv, int d, int topk) {
-  if (nseq < 1 || T < 1 || (d != 64 && d != 128)) return 0;
+size_t misa_paged_attention_workspace_size(int nseq, int T, int Hq, int Hkv, int d, int page_size,
+                                           int max_pages, int topk) {
+  if (nseq < 1 || T < 1 || (d != 64 && d != 128) || page_size < 1 || max_pages < 1) return 0;
   if (check_heads(nseq, T, Hq, Hkv, topk) != MISA_OK) return 0;
   PagedAttn p = {};
   p.nseq = nseq;
@@ -102,6 +104,8 @@ size_t misa_paged_attention_workspace_size(int nseq, int T, int Hq, int Hkv, int
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.d = d;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
   p.topk = topk;
   return paged_attn_ws_bytes(p);
 }
@@ -151,11 +155,17 @@ int misa_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
                                          device_status, (cudaStream_t)stream));
 }
 
-size_t misa_pages_workspace_size(int nseq, int max_pages, int num_pages) {
+size_t misa_pages_workspace_size(int op, int nseq, int max_pages, int num_pages) {
   if (check_table(nseq, max_pages, num_pages) != MISA_OK) return 0;
-  const size_t plan = pages_ws_bytes(nseq, num_pages);
-  const size_t table = align256((size_t)nseq * max_pages * 4);   // a fork in place
-  return plan > table ? plan : table;
+  switch (op) {
+    case MISA_OP_PAGES_RESIZE:
+    case MISA_OP_PAGES_COMPACT:
+      return pages_ws_bytes(nseq, num_pages);
+    case MISA_OP_PAGES_FORK:
+      return fork_ws_bytes(nseq, max_pages, num_pages);
+    default:
+      return 0;
+  }
 }
 
 int misa_pages_resize(const int32_t* page_table, const int32_t* refs, const int32_t* old_len,
@@ -166,8 +176,8 @@ int misa_pages_resize(const int32_t* page_table, const int32_t* refs, const int3
   MISA_TRY(check_table(nseq, max_pages, num_pages));
   if (page_size < 1) return MISA_ERR_INVALID_ARG;
   if ((int64_t)max_pages * page_size > kMaxSpan) return MISA_ERR_UNSUPPORTED;
-  MISA_TRY(check_upkeep(page_table, refs, nseq, max_pages, num_pages, out_table, out_refs, ws,
-                        ws_bytes));
+  MISA_TRY(check_upkeep(MISA_OP_PAGES_RESIZE, page_table, refs, nseq, max_pages, num_pages, out_table,
+                        out_refs, ws, ws_bytes));
   MISA_TRY(check_dev(old_len, (size_t)nseq * 4, 4));
   MISA_TRY(check_dev(new_len, (size_t)nseq * 4, 4));
   MISA_TRY(check_opt(device_status, 4, 4));
@@ -183,8 +193,8 @@ int misa_pages_fork(const int32_t* page_table, const int32_t* refs, const int32_
                     int32_t* out_refs, int32_t* device_status, void* ws, size_t ws_bytes,
                     void* stream) {
   MISA_TRY(check_table(nseq, max_pages, num_pages));
-  MISA_TRY(check_upkeep(page_table, refs, nseq, max_pages, num_pages, out_table, out_refs, ws,
-                        ws_bytes));
+  MISA_TRY(check_upkeep(MISA_OP_PAGES_FORK, page_table, refs, nseq, max_pages, num_pages, out_table,
+                        out_refs, ws, ws_bytes));
   MISA_TRY(check_dev(parent, (size_t)nseq * 4, 4));
   MISA_TRY(check_opt(device_status, 4, 4));
   return cuda_status(launch_pages_fork(page_table, refs, parent, nseq, max_pages, num_pages,
@@ -197,8 +207,8 @@ int misa_pages_compact(const int32_t* page_table, const int32_t* refs, int nseq,
                        int32_t* out_table, int32_t* out_refs, int32_t* n_live,
                        int32_t* device_status, void* ws, size_t ws_bytes, void* stream) {
   MISA_TRY(check_table(nseq, max_pages, num_pages));
-  MISA_TRY(check_upkeep(page_table, refs, nseq, max_pages, num_pages, out_table, out_refs, ws,
-                        ws_bytes));
+  MISA_TRY(check_upkeep(MISA_OP_PAGES_COMPACT, page_table, refs, nseq, max_pages, num_pages, out_table,
+                        out_refs, ws, ws_bytes));
   MISA_TRY(check_opt(n_live, 4, 4));
   MISA_TRY(check_opt(device_status, 4, 4));
   PagePools pp;

@@ -205,7 +205,8 @@ struct PagePools {
   unsigned char* base[MISA_MAX_POOLS];
   uint32_t page_bytes[MISA_MAX_POOLS];   // multiples of 16
 };
-size_t pages_ws_bytes(int nseq, int num_pages);
+size_t pages_ws_bytes(int nseq, int num_pages);   // resize and compact
+size_t fork_ws_bytes(int nseq, int max_pages, int num_pages);
 cudaError_t launch_pages_resize(const int32_t* table, const int32_t* refs, const int32_t* old_len,
                                 const int32_t* new_len, int nseq, int max_pages, int num_pages,
                                 int page_size, const PagePools& pools, int32_t* out_table,

@@ -13,6 +13,22 @@
 namespace misa {
 namespace paged {
 
+// n / d of 0 <= n < 2^31 by a multiplication: with l = ceil(log2 d), (umulhi(n, mul) + n) >> l for
+// mul = floor(2^32 (2^l - d) / d) + 1 (Granlund and Montgomery).
+struct Divide {
+  uint32_t mul, shift;
+  static Divide by(int divisor) {
+    const uint32_t d = (uint32_t)divisor;
+    Divide x = {0, 0};
+    while ((uint64_t(1) << x.shift) < d) ++x.shift;
+    x.mul = (uint32_t)((((uint64_t(1) << x.shift) - d) << 32) / d + 1);
+    return x;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+  }
+};
+
 // Two fp32 values rounded to the 16-bit type, `lo` in the lower half.
 template <typename E>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
@@ -103,8 +119,8 @@ __device__ __forceinline__ int last_token(const int32_t* __restrict__ pos, int64
 // -1 (reported) when the page entry names no page of the pool.  The pool holds fewer than 2^31
 // rows.
 __device__ __forceinline__ int cache_row(const int32_t* __restrict__ pages, int s, int page_size,
-                                         int num_pages, int* status) {
-  const int i = s / page_size;
+                                         const Divide& by_page, int num_pages, int* status) {
+  const int i = by_page(s);
   const int page = __ldg(pages + i);
   if ((unsigned)page >= (unsigned)num_pages) {
     set_status(status, MISA_ERR_BAD_DEVICE_INPUT);

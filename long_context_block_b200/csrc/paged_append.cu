@@ -17,19 +17,20 @@ constexpr int kAppendThreads = 256;
 
 // blockIdx.y: 0 keys, 1 values.  `per_row`: 16-byte pieces of a row.
 template <int U>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 6)
     paged_append_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
                         const int32_t* __restrict__ pos, const int32_t* __restrict__ table, int T,
-                        int64_t pieces, int per_row, int num_pages, int page_size, int max_pages,
+                        int64_t pieces, int per_row, int num_pages, int page_size, Divide by_page,
+                        int max_pages,
                         uint4* __restrict__ k_cache, uint4* __restrict__ v_cache, int* status) {
   pdl_prologue();
   const uint4* src = blockIdx.y ? v_new : k_new;
   uint4* dst = blockIdx.y ? v_cache : k_cache;
   const int64_t base = (int64_t)blockIdx.x * (kAppendThreads * U);
-  const int64_t row0 = base / per_row;
-  const int rem = (int)(base - row0 * per_row);
+  const int row0 = (int)(base / per_row);
+  const int rem = (int)(base - (int64_t)row0 * per_row);
   uint4 x[U];
-  int64_t row[U];
+  int row[U];
   int c[U], p[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     c[u] = at % per_row;
     p[u] = -1;
     if (base + u * kAppendThreads + (int)threadIdx.x < pieces) {
-      x[u] = __ldcs(src + row[u] * per_row + c[u]);
+      x[u] = __ldcs(src + base + u * kAppendThreads + threadIdx.x);
       p[u] = last_token(pos, row[u], max_pages * page_size, status);
       // a position past the table's last page has no place: skipped, not clamped onto another
       if (p[u] != pos[row[u]]) p[u] = -1;
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 #pragma unroll
   for (int u = 0; u < U; ++u)
     at[u] = p[u] < 0 ? -1
-                     : cache_row(table + (int64_t)((int)row[u] / T) * max_pages, p[u], page_size, num_pages, status);
+                     : cache_row(table + (int64_t)(row[u] / T) * max_pages, p[u], page_size, by_page, num_pages, status);
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (at[u] >= 0) dst[(int64_t)at[u] * per_row + c[u]] = x[u];
@@ -70,7 +71,7 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int3
   return launch_pdl(wide ? paged_append_kernel<4> : paged_append_kernel<1>,
                     dim3((unsigned)blocks, 2), dim3(kAppendThreads), 0, st,
                     static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), pos,
-                    page_table, T, pieces, per_row, num_pages, page_size, max_pages,
+                    page_table, T, pieces, per_row, num_pages, page_size, Divide::by(page_size), max_pages,
                     static_cast<uint4*>(k_cache), static_cast<uint4*>(v_cache), status);
 }
 

@@ -11,11 +11,18 @@
 // queries of a draft) share each loaded tile, and keeps the running maximum, sum and output in
 // registers; the CTA's warps are joined at the end of a segment.
 //
-// Split: the units (64 or 128 tokens of one item = row block x key-value head) of all items are
-// laid end to end and cut into one equal range per CTA, whatever the lengths are.  An item that
-// spans CTAs leaves fp32 partials (at most two per CTA), joined by paged_join_kernel in the order
-// of the CTAs, so results do not depend on timing.
+// Split, two ways:
+//   - shared items (paged_attn_cluster_kernel): one thread-block cluster per item (row block x
+//     key-value head) whose CTAs take equal parts of its tokens and join over distributed shared
+//     memory: one launch, no scratch.
+//   - equal ranges (paged_attn_kernel): the units (64 or 128 tokens) of all items are laid end to
+//     end and cut into one equal range per CTA, whatever the lengths are.  An item that spans
+//     CTAs leaves fp32 partials (at most two per CTA), joined by paged_join_kernel.
+// Both join in a fixed order, so results do not depend on timing.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
+
+#include <cmath>
 
 #include "internal.h"
 #include "misa.h"
@@ -25,6 +32,7 @@ namespace misa {
 namespace {
 
 using namespace paged;
+namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -32,6 +40,11 @@ constexpr int kStages = 3;
 // Two CTAs per SM (148 SMs): also what bounds the partials, so the workspace does not depend on
 // the lengths.
 constexpr int kMaxCtas = 296;
+constexpr int kMaxCluster = 8;     // the largest portable cluster
+// CTAs of larger clusters than pairs that are resident at once: a cluster stays within one group
+// of SMs, which leaves 264 to 284 of the 296 places (cudaOccupancyMaxActiveClusters, sizes 3 - 8).
+constexpr int kClusterCtas = 256;
+constexpr int kClusterUnits = 16;  // units per CTA up to which a cluster shares an item
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -51,7 +64,10 @@ struct AttnArgs {
                    // and the CTA it ends in
   int nseq, T, Hq, Hkv, G, num_pages, page_size, max_pages, topk;
   int nb;          // row blocks: per sequence (prefix form) or per query (selected form)
-  float scale2;    // scale * log2 e
+  float scale2;    // |scale| log2 e, or 1 with queries of zeros
+  uint32_t q_flip; // sign bits of a query's word to flip (scale < 0)
+  uint32_t q_keep; // bits of a query's word to keep (none: scale = 0)
+  Divide by_page;  // division by page_size
 };
 
 // An entry is a row block: of a sequence's T * G rows (prefix form, r = t * G + g) or of one
@@ -82,40 +98,420 @@ struct Entry {
   }
 };
 
+template <int D, int MT>
+struct Shape {
+  static constexpr int RB = 16 * MT;      // query rows of an item
+  static constexpr int KT = 2048 / D;     // tokens of a warp's tile
+  static constexpr int UNIT = kWarps * KT;
+  static constexpr int ROWB = D * 2;      // bytes of a key or value row
+  static constexpr int CH = ROWB / 16;    // 16-byte chunks of a row
+  static constexpr int TILE = KT * ROWB;  // bytes of a key (or value) tile
+  static constexpr int RING = kWarps * kStages * 2 * TILE;
+  static constexpr int OSTR = D + 8;      // row stride of the join buffer (no bank conflicts)
+  static constexpr int SMEM = RING + RB * ROWB;
+  static_assert(kWarps * RB * OSTR * 4 <= RING, "the join buffer lies in the ring");
+};
+
+// One output position: 4 elements of a row, from its sum of weights and weighted values.
+template <typename E, int D>
+__device__ __forceinline__ void finish(const AttnArgs& a, int n, int rr, int hk, int c,
+                                       const float4& acc, float mm, float ll) {
+  const int t = rr / a.G, g = rr - t * a.G;
+  const int64_t head = ((int64_t)n * a.T + t) * a.Hq + hk * a.G + g;
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;
+  uint2 y;
+  y.x = pack2<E>(acc.x * inv, acc.y * inv);
+  y.y = pack2<E>(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(static_cast<E*>(a.out) + head * D + c) = y;
+  if (a.lse && c == 0) a.lse[head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+}
+
+// Adds a part (maximum pm, sum pl, weighted values x) under the joint maximum mm.
+__device__ __forceinline__ void add_part(float4& acc, float& ll, float mm, float pm, float pl,
+                                         const float4& x) {
+  const float f = pm == mm ? 1.f : exp2_approx(pm - (mm == -INFINITY ? 0.f : mm));
+  ll += pl * f;
+  acc.x += x.x * f;
+  acc.y += x.y * f;
+  acc.z += x.z * f;
+  acc.w += x.w * f;
+}
+
+// Tokens tok0 .. tok1 - 1 of entry `en` (of the prefix, or slots of its idx row) for key-value
+// head hk, by the whole CTA.  Leaves each warp's part in shared memory: weighted values at
+// smem (rows of OSTR floats, warp-major), maximum and sum in s_ml.
 template <typename E, int D, int MT, bool SEL>
-__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs a) {
-  constexpr int RB = 16 * MT;             // query rows of an item
-  constexpr int KT = 2048 / D;            // tokens of a warp's tile
-  constexpr int UNIT = kWarps * KT;
-  constexpr int ROWB = D * 2;             // bytes of a key or value row
-  constexpr int CH = ROWB / 16;           // 16-byte chunks of a row
+__device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, SEL>& en, int hk,
+                                       int tok0, int tok1, unsigned char* smem,
+                                       float2 (*s_ml)[16 * MT]) {
+  using S = Shape<D, MT>;
+  constexpr int RB = S::RB, KT = S::KT, UNIT = S::UNIT, ROWB = S::ROWB, CH = S::CH,
+                TILE = S::TILE;
   constexpr int NT = KT / 8;              // 8-token columns of a score tile
   constexpr int DN = D / 8;               // 8-wide columns of the output
-  constexpr int TILE = KT * ROWB;         // bytes of a key (or value) tile
-  constexpr int OSTR = D + 8;             // row stride of the join buffer (no bank conflicts)
-  static_assert(kWarps * RB * OSTR * 4 <= kWarps * kStages * 2 * TILE, "join buffer");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned char* s_q = smem + S::RING;
+  const uint32_t ring = sm100::smem_u32(smem) + warp * (kStages * 2 * TILE);
+  const uint32_t qbase = sm100::smem_u32(s_q);
+  const int cap = a.max_pages * a.page_size;
+  const int32_t* pages = a.table + (int64_t)en.n * a.max_pages;
+  const int64_t sel_row = (int64_t)en.n * a.T + en.row0 / a.G;   // selected form: the query
+  const int32_t* ids = SEL ? a.idx + sel_row * a.topk : nullptr;
+
+  // ---- tile i of this warp starts at token tok0 + (i * kWarps + warp) * KT
+  const int first = tok0 + warp * KT;
+  const int ntile = first < tok1 ? (tok1 - first + UNIT - 1) / UNIT : 0;
+  // What a lane looks up for its token of a tile is read ahead of its use, a tile per step:
+  // the token id (selected form), then its page entry, then the copy.
+  auto token = [&](int i) -> int {
+    const int s = first + i * UNIT + lane;
+    if (lane >= KT || i >= ntile || s >= tok1) return -1;
+    return SEL ? __ldg(ids + s) : s;
+  };
+  int last_sel = -1;
+  auto page_of = [&](int tok, int& page, int& in_page) {
+    page = in_page = -1;
+    if (SEL && (tok < -1 || tok > last_sel)) {
+      set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
+      tok = -1;
+    }
+    if (tok < 0) return;
+    const int i = a.by_page(tok);
+    page = __ldg(pages + i);
+    in_page = tok - i * a.page_size;
+  };
+  const char* kb = static_cast<const char*>(a.k) + hk * ROWB + (lane % CH) * 16;
+  const char* vb = static_cast<const char*>(a.v) + hk * ROWB + (lane % CH) * 16;
+  const int64_t tstride = (int64_t)a.Hkv * ROWB;
+  // copy the tile whose page entries the lanes hold; returns the tokens that are there
+  auto issue = [&](int i, int page, int in_page) -> uint32_t {
+    int row = -1;
+    if (in_page >= 0) {
+      if ((unsigned)page < (unsigned)a.num_pages)
+        row = page * a.page_size + in_page;
+      else
+        set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
+    }
+    const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+    if (live) {
+      const uint32_t dst = ring + (i % kStages) * (2 * TILE);
+      constexpr int PER = 32 / CH;   // rows of one warp-wide copy
+#pragma unroll
+      for (int j = 0; j < KT / PER; ++j) {
+        const int r = j * PER + lane / CH;
+        const int src = __shfl_sync(0xffffffffu, row, r);
+        const bool ok = src >= 0;
+        const int64_t at = ok ? src * tstride : 0;
+        const uint32_t d = dst + r * ROWB + (((lane % CH) ^ (r & 7)) << 4);
+        cp_async16_or_zero(d, kb + at, ok);
+        cp_async16_or_zero(d + TILE, vb + at, ok);
+      }
+    }
+    cp_async_commit();
+    return live;
+  };
+  // The first tiles' lookups go together, so that they cost one latency per step, not per tile.
+  int tok[kStages];
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) tok[i] = token(i);
+  if (SEL) last_sel = last_token(a.pos, sel_row, cap, a.status);
+  int pages_at[kStages], in_pages[kStages];
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) page_of(tok[i], pages_at[i], in_pages[i]);
+  int page = pages_at[kStages - 1], in_page = in_pages[kStages - 1], tok_next = token(kStages);
+  uint32_t live[kStages];
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) live[i] = issue(i, pages_at[i], in_pages[i]);
+
+  // ---- the query rows, zero behind the last one, while the first tiles are on their way
+  {
+    const E* q = static_cast<const E*>(a.q);
+    for (int i = tid; i < RB * CH; i += kThreads) {
+      const int r = i / CH, c = i - r * CH;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < en.rows) {
+        const int rr = en.row0 + r, t = rr / a.G, g = rr - t * a.G;
+        x = *reinterpret_cast<const uint4*>(
+            q + (((int64_t)en.n * a.T + t) * a.Hq + hk * a.G + g) * D + c * 8);
+        x.x = (x.x ^ a.q_flip) & a.q_keep;
+        x.y = (x.y ^ a.q_flip) & a.q_keep;
+        x.z = (x.z ^ a.q_flip) & a.q_keep;
+        x.w = (x.w ^ a.q_flip) & a.q_keep;
+      }
+      *reinterpret_cast<uint4*>(s_q + r * ROWB + ((c ^ (r & 7)) << 4)) = x;
+    }
+  }
+  // last visible token of this thread's rows
+  int lim[2 * MT];
+  int lim_min = cap;
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i) {
+    const int r = (lane >> 2) + 8 * i;
+    lim[i] = cap;
+    if (!SEL && r < en.rows) {
+      lim[i] = last_token(a.pos, (int64_t)en.n * a.T + (en.row0 + r) / a.G, cap, nullptr);
+      lim_min = min(lim_min, lim[i]);
+    }
+  }
+  __syncthreads();
+
+  float o[MT][DN][4];
+  float m[2 * MT], l[2 * MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < DN; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[mt][i][x] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+  }
+  uint32_t qf[MT == 1 ? D / 16 : 1][4];
+  const int arow = (lane & 7) + ((lane >> 3) & 1) * 8;
+  if constexpr (MT == 1) {
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      ldmatrix4(qf[kk], qbase + arow * ROWB + (((2 * kk + (lane >> 4)) ^ (lane & 7)) << 4));
+  }
+
+  for (int i = 0; i < ntile; ++i) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    live[kStages - 1] = issue(i + kStages - 1, page, in_page);
+    page_of(tok_next, page, in_page);
+    tok_next = token(i + kStages + 1);
+    const uint32_t ok = live[0];
+#pragma unroll
+    for (int j = 0; j + 1 < kStages; ++j) live[j] = live[j + 1];
+    if (ok == 0) continue;
+    const uint32_t kt = ring + (i % kStages) * (2 * TILE), vt = kt + TILE;
+
+    float s[MT][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int x = 0; x < NT; ++x) s[mt][x][0] = s[mt][x][1] = s[mt][x][2] = s[mt][x][3] = 0.f;
+    const int brow = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t qa[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if constexpr (MT == 1) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) qa[mt][x] = qf[kk][x];
+        } else {
+          ldmatrix4(qa[mt], qbase + (mt * 16 + arow) * ROWB +
+                                (((2 * kk + (lane >> 4)) ^ (lane & 7)) << 4));
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < NT / 2; ++p) {
+        uint32_t b[4];
+        ldmatrix4(b, kt + (p * 16 + brow) * ROWB +
+                         (((2 * kk + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<E>(s[mt][2 * p], qa[mt], b[0], b[1]);
+          mma16816<E>(s[mt][2 * p + 1], qa[mt], b[2], b[3]);
+        }
+      }
+    }
+
+    // what a row does not see is -inf
+    const int s0 = first + i * UNIT;
+    const uint32_t full = KT == 32 ? 0xffffffffu : (1u << KT) - 1u;
+    if (ok != full || (!SEL && s0 + KT - 1 > lim_min)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int c = x * 8 + (lane & 3) * 2 + (y & 1);
+            const bool see = ((ok >> c) & 1u) && (SEL || s0 + c <= lim[2 * mt + (y >> 1)]);
+            if (!see) s[mt][x][y] = -INFINITY;
+          }
+    }
+    // the running maximum is kept in the log2 domain: m = max of the scores * scale2 (> 0)
+    float mx[2 * MT];
+    bool up = false;
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) {
+      float t = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+        t = fmaxf(t, fmaxf(s[r >> 1][x][(r & 1) * 2], s[r >> 1][x][(r & 1) * 2 + 1]));
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+      mx[r] = fmaxf(m[r], t * a.scale2);
+      up |= mx[r] > m[r];
+    }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int r = 0; r < 2 * MT; ++r) {
+        const float f = mx[r] == m[r] ? 1.f : exp2_approx(m[r] - mx[r]);
+        m[r] = mx[r];
+        l[r] *= f;
+#pragma unroll
+        for (int x = 0; x < DN; ++x) {
+          o[r >> 1][x][(r & 1) * 2] *= f;
+          o[r >> 1][x][(r & 1) * 2 + 1] *= f;
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) {
+      const float base = m[r] == -INFINITY ? 0.f : -m[r];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float& p = s[r >> 1][x][(r & 1) * 2 + y];
+          p = exp2_approx(fmaf(p, a.scale2, base));
+          l[r] += p;
+        }
+    }
+    const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+    for (int ks = 0; ks < NT / 2; ++ks) {
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        pa[mt][0] = pack2<E>(s[mt][2 * ks][0], s[mt][2 * ks][1]);
+        pa[mt][1] = pack2<E>(s[mt][2 * ks][2], s[mt][2 * ks][3]);
+        pa[mt][2] = pack2<E>(s[mt][2 * ks + 1][0], s[mt][2 * ks + 1][1]);
+        pa[mt][3] = pack2<E>(s[mt][2 * ks + 1][2], s[mt][2 * ks + 1][3]);
+      }
+#pragma unroll
+      for (int p = 0; p < DN / 2; ++p) {
+        uint32_t b[4];
+        ldmatrix4_trans(b, vt + (ks * 16 + vrow) * ROWB +
+                               (((2 * p + (lane >> 4)) ^ (lane & 7)) << 4));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<E>(o[mt][2 * p], pa[mt], b[0], b[1]);
+          mma16816<E>(o[mt][2 * p + 1], pa[mt], b[2], b[3]);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();   // every warp is done with its ring
+
+  float* s_o = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int r = 0; r < 2 * MT; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    const int row = (lane >> 2) + 8 * r;
+    if ((lane & 3) == 0) s_ml[warp][row] = make_float2(m[r], l[r]);
+#pragma unroll
+    for (int x = 0; x < DN; ++x)
+      *reinterpret_cast<float2*>(s_o + (warp * RB + row) * S::OSTR + x * 8 + (lane & 3) * 2) =
+          make_float2(o[r >> 1][x][(r & 1) * 2], o[r >> 1][x][(r & 1) * 2 + 1]);
+  }
+  __syncthreads();
+}
+
+// The CTA's sum over its warps at row r, elements c .. c + 3.
+template <int D, int MT>
+__device__ __forceinline__ float4 warp_sum(const unsigned char* smem,
+                                           const float2 (*s_ml)[16 * MT], int r, int c, float& mm,
+                                           float& ll) {
+  using S = Shape<D, MT>;
+  const float* s_o = reinterpret_cast<const float*>(smem);
+  mm = -INFINITY;
+  ll = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][r].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    add_part(acc, ll, mm, s_ml[w][r].x, s_ml[w][r].y,
+             *reinterpret_cast<const float4*>(s_o + (w * S::RB + r) * S::OSTR + c));
+  return acc;
+}
+
+template <typename E, int D, int MT, bool SEL>
+__global__ void __launch_bounds__(kThreads, 2) paged_attn_cluster_kernel(const AttnArgs a) {
+  using S = Shape<D, MT>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ float2 s_ml[kWarps][S::RB];
+  __shared__ float2 s_part[S::RB];
+  pdl_prologue();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int item = blockIdx.x / size, hk = item % a.Hkv;
+  const Entry<S::RB, SEL> en(a, item / a.Hkv);
+  const int ntok = en.tokens(a);
+  const int64_t units = (ntok + S::UNIT - 1) / S::UNIT;
+  attend<E, D, MT, SEL>(a, en, hk, (int)(rank * units / size) * S::UNIT,
+                        min(ntok, (int)((rank + 1) * units / size) * S::UNIT), smem, s_ml);
+  float* s_o = reinterpret_cast<float*>(smem);
+  const int work = en.rows * (D / 4);
+  if (size > 1) {   // this CTA's sum takes the place of its first warp's part
+    for (int i = threadIdx.x; i < work; i += kThreads) {
+      const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+      float mm, ll;
+      const float4 acc = warp_sum<D, MT>(smem, s_ml, r, c, mm, ll);
+      *reinterpret_cast<float4*>(s_o + r * S::OSTR + c) = acc;
+      if (c == 0) s_part[r] = make_float2(mm, ll);
+    }
+    cluster.sync();
+  }
+  for (int i = rank * kThreads + threadIdx.x; i < work; i += size * kThreads) {
+    const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+    float mm = -INFINITY, ll = 0.f;
+    float4 acc;
+    if (size > 1) {
+      float2 ml[kMaxCluster];
+      float4 x[kMaxCluster];
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p)   // all reads at once
+        if (p < size) {
+          ml[p] = cluster.map_shared_rank(s_part, p)[r];
+          x[p] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(s_o, p) + r * S::OSTR + c);
+        }
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p)
+        if (p < size) mm = fmaxf(mm, ml[p].x);
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p)
+        if (p < size) add_part(acc, ll, mm, ml[p].x, ml[p].y, x[p]);
+    } else {
+      acc = warp_sum<D, MT>(smem, s_ml, r, c, mm, ll);
+    }
+    finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
+  }
+  if (size > 1) cluster.sync();   // no CTA leaves while another reads its shared memory
+}
+
+template <typename E, int D, int MT, bool SEL>
+__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs a) {
+  using S = Shape<D, MT>;
+  constexpr int RB = S::RB, UNIT = S::UNIT;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ float2 s_ml[kWarps][RB];
   __shared__ long long s_red[kWarps];
   __shared__ int s_entry;
   __shared__ long long s_off;
-  unsigned char* s_q = smem + kWarps * kStages * 2 * TILE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_prologue();
 
   // ---- this CTA's range of units
   const int ne = (SEL ? a.nseq * a.T : a.nseq) * a.nb;
   const int chunk = (ne + kThreads - 1) / kThreads;
-  long long mine = 0, total, before;
-  int e = 0;
-  long long off = 0, u0, u1;
-  if (SEL) {
-    total = (long long)ne * a.Hkv * ((a.topk + UNIT - 1) / UNIT);
-    before = 0;
-  } else {
-    for (int i = tid * chunk; i < min(ne, (tid + 1) * chunk); ++i)
-      mine += max(1, (Entry<RB, SEL>(a, i).tokens(a) + UNIT - 1) / UNIT);
-    mine *= a.Hkv;
+  const int per = SEL ? (a.topk + UNIT - 1) / UNIT * a.Hkv : 0;   // units of an entry
+  auto units_of = [&](int i) {
+    return max(1, (Entry<RB, SEL>(a, i).tokens(a) + UNIT - 1) / UNIT) * a.Hkv;
+  };
+  long long mine = 0, before = 0, total = (long long)ne * per;
+  if (!SEL) {
+    for (int i = tid * chunk; i < min(ne, (tid + 1) * chunk); ++i) mine += units_of(i);
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -125,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs 
     if (lane == 31) s_red[warp] = inc;
     __syncthreads();
     before = inc - mine;
-    total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += s_red[w];
@@ -138,345 +533,53 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs 
     if (tid == 0) a.split[cta] = make_int2(-1, 0);
     return;
   }
-  u0 = cta * total / nc;
-  u1 = (cta + 1) * total / nc;
-  if (SEL) {
-    const int per = a.Hkv * ((a.topk + UNIT - 1) / UNIT);
+  const long long u0 = cta * total / nc, u1 = (cta + 1) * total / nc;
+  int e;
+  long long off;   // units of entry e before u
+  if constexpr (SEL) {
     e = (int)(u0 / per);
     off = u0 - (long long)e * per;
   } else {
-    if (mine > 0 && u0 >= before && u0 < before + mine) {
-      long long o = u0 - before;
-      int i = tid * chunk;
-      while (true) {
-        const int u = max(1, (Entry<RB, SEL>(a, i).tokens(a) + UNIT - 1) / UNIT) * a.Hkv;
-        if (o < u) break;
-        o -= u;
-        ++i;
+    if (u0 >= before && u0 < before + mine) {
+      off = u0 - before;
+      e = tid * chunk;
+      for (int u = units_of(e); off >= u; u = units_of(e)) {
+        off -= u;
+        ++e;
       }
-      s_entry = i;
-      s_off = o;
+      s_entry = e;
+      s_off = off;
     }
     __syncthreads();
     e = s_entry;
     off = s_off;
   }
 
-  const uint32_t ring = sm100::smem_u32(smem) + warp * (kStages * 2 * TILE);
-  const uint32_t qbase = sm100::smem_u32(s_q);
-  const int cap = a.max_pages * a.page_size;
   int2 split = make_int2(-1, 0);
-
   for (long long u = u0; u < u1;) {
     const Entry<RB, SEL> en(a, e);
     const int ntok = en.tokens(a);
     const int units = max(1, (ntok + UNIT - 1) / UNIT);
     const int hk = (int)(off / units), uo = (int)(off - (long long)hk * units);
     const int take = (int)min((long long)(units - uo), u1 - u);
-    const int tok0 = uo * UNIT;
-    const int tok1 = min(ntok, (uo + take) * UNIT);
-    const int32_t* pages = a.table + (int64_t)en.n * a.max_pages;
-    const int32_t* ids = nullptr;
-    int last_sel = -1;
-    if (SEL) {
-      const int64_t row = (int64_t)en.n * a.T + en.row0 / a.G;
-      ids = a.idx + row * a.topk;
-      last_sel = last_token(a.pos, row, cap, a.status);
-    }
-
-    // ---- the query rows, zero behind the last one
-    __syncthreads();   // the previous segment's join has read the buffers
-    {
-      const E* q = static_cast<const E*>(a.q);
-      for (int i = tid; i < RB * CH; i += kThreads) {
-        const int r = i / CH, c = i - r * CH;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < en.rows) {
-          const int rr = en.row0 + r, t = rr / a.G, g = rr - t * a.G;
-          x = *reinterpret_cast<const uint4*>(
-              q + (((int64_t)en.n * a.T + t) * a.Hq + hk * a.G + g) * D + c * 8);
-        }
-        *reinterpret_cast<uint4*>(s_q + r * ROWB + ((c ^ (r & 7)) << 4)) = x;
-      }
-    }
-    // last visible token of this thread's rows
-    int lim[2 * MT];
-    int lim_min = cap;
-#pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
-      const int r = (lane >> 2) + 8 * i;
-      lim[i] = cap;
-      if (!SEL && r < en.rows) {
-        lim[i] = last_token(a.pos, (int64_t)en.n * a.T + (en.row0 + r) / a.G, cap, nullptr);
-        lim_min = min(lim_min, lim[i]);
-      }
-    }
-    __syncthreads();
-
-    float o[MT][DN][4];
-    float m[2 * MT], l[2 * MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i = 0; i < DN; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[mt][i][x] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-    }
-    uint32_t qf[MT == 1 ? D / 16 : 1][4];
-    const int arow = (lane & 7) + ((lane >> 3) & 1) * 8;
-    if constexpr (MT == 1) {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        ldmatrix4(qf[kk], qbase + arow * ROWB + (((2 * kk + (lane >> 4)) ^ (lane & 7)) << 4));
-    }
-
-    // ---- tile i of this warp starts at token tok0 + (i * kWarps + warp) * KT
-    const int first = tok0 + warp * KT;
-    const int ntile = first < tok1 ? (tok1 - first + UNIT - 1) / UNIT : 0;
-    // What a lane looks up for its token of a tile is read ahead of its use, a tile per step:
-    // the token id (selected form), then its page entry, then the copy.
-    auto token = [&](int i) -> int {
-      const int s = first + i * UNIT + lane;
-      if (lane >= KT || i >= ntile || s >= tok1) return -1;
-      return SEL ? __ldg(ids + s) : s;
-    };
-    auto page_of = [&](int tok, int& page, int& in_page) {
-      in_page = -1;
-      if (SEL && (tok < -1 || tok > last_sel)) {
-        set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
-        tok = -1;
-      }
-      if (tok < 0) return;
-      const int i = tok / a.page_size;
-      page = __ldg(pages + i);
-      in_page = tok - i * a.page_size;
-    };
-    const char* kb = static_cast<const char*>(a.k) + hk * ROWB + (lane % CH) * 16;
-    const char* vb = static_cast<const char*>(a.v) + hk * ROWB + (lane % CH) * 16;
-    const int64_t tstride = (int64_t)a.Hkv * ROWB;
-    // copy the tile whose page entries the lanes hold; returns the tokens that are there
-    auto issue = [&](int i, int page, int in_page) -> uint32_t {
-      int row = -1;
-      if (in_page >= 0) {
-        if ((unsigned)page < (unsigned)a.num_pages)
-          row = page * a.page_size + in_page;
-        else
-          set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
-      }
-      const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
-      if (live) {
-        const uint32_t dst = ring + (i % kStages) * (2 * TILE);
-        constexpr int PER = 32 / CH;   // rows of one warp-wide copy
-#pragma unroll
-        for (int j = 0; j < KT / PER; ++j) {
-          const int r = j * PER + lane / CH;
-          const int src = __shfl_sync(0xffffffffu, row, r);
-          const bool ok = src >= 0;
-          const int64_t at = ok ? src * tstride : 0;
-          const uint32_t d = dst + r * ROWB + (((lane % CH) ^ (r & 7)) << 4);
-          cp_async16_or_zero(d, kb + at, ok);
-          cp_async16_or_zero(d + TILE, vb + at, ok);
-        }
-      }
-      cp_async_commit();
-      return live;
-    };
-
-    uint32_t live[kStages];
-    int page = -1, in_page, tok_next = token(1);
-    page_of(token(0), page, in_page);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      live[i] = issue(i, page, in_page);
-      page_of(tok_next, page, in_page);
-      tok_next = token(i + 2);
-    }
-    for (int i = 0; i < ntile; ++i) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      live[kStages - 1] = issue(i + kStages - 1, page, in_page);
-      page_of(tok_next, page, in_page);
-      tok_next = token(i + kStages + 1);
-      const uint32_t ok = live[0];
-#pragma unroll
-      for (int j = 0; j + 1 < kStages; ++j) live[j] = live[j + 1];
-      if (ok == 0) continue;
-      const uint32_t kt = ring + (i % kStages) * (2 * TILE), vt = kt + TILE;
-
-      float s[MT][NT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int x = 0; x < NT; ++x) s[mt][x][0] = s[mt][x][1] = s[mt][x][2] = s[mt][x][3] = 0.f;
-      const int brow = (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t qa[MT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          if constexpr (MT == 1) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) qa[mt][x] = qf[kk][x];
-          } else {
-            ldmatrix4(qa[mt], qbase + (mt * 16 + arow) * ROWB +
-                                  (((2 * kk + (lane >> 4)) ^ (lane & 7)) << 4));
-          }
-        }
-#pragma unroll
-        for (int p = 0; p < NT / 2; ++p) {
-          uint32_t b[4];
-          ldmatrix4(b, kt + (p * 16 + brow) * ROWB +
-                           (((2 * kk + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816<E>(s[mt][2 * p], qa[mt], b[0], b[1]);
-            mma16816<E>(s[mt][2 * p + 1], qa[mt], b[2], b[3]);
-          }
-        }
-      }
-
-      // scores in the log2 domain; what a row does not see is -inf
-      const int s0 = first + i * UNIT;
-      const uint32_t full = KT == 32 ? 0xffffffffu : (1u << KT) - 1u;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) s[mt][x][y] *= a.scale2;
-      if (ok != full || (!SEL && s0 + KT - 1 > lim_min)) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int x = 0; x < NT; ++x)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int c = x * 8 + (lane & 3) * 2 + (y & 1);
-              const bool see = ((ok >> c) & 1u) && (SEL || s0 + c <= lim[2 * mt + (y >> 1)]);
-              if (!see) s[mt][x][y] = -INFINITY;
-            }
-      }
-      float mx[2 * MT];
-      bool up = false;
-#pragma unroll
-      for (int r = 0; r < 2 * MT; ++r) {
-        float t = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-          t = fmaxf(t, fmaxf(s[r >> 1][x][(r & 1) * 2], s[r >> 1][x][(r & 1) * 2 + 1]));
-        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-        mx[r] = fmaxf(m[r], t);
-        up |= mx[r] > m[r];
-      }
-      if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-        for (int r = 0; r < 2 * MT; ++r) {
-          const float f = mx[r] == m[r] ? 1.f : exp2_approx(m[r] - mx[r]);
-          m[r] = mx[r];
-          l[r] *= f;
-#pragma unroll
-          for (int x = 0; x < DN; ++x) {
-            o[r >> 1][x][(r & 1) * 2] *= f;
-            o[r >> 1][x][(r & 1) * 2 + 1] *= f;
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 2 * MT; ++r) {
-        const float base = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float& p = s[r >> 1][x][(r & 1) * 2 + y];
-            p = exp2_approx(p - base);
-            l[r] += p;
-          }
-      }
-      const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-      for (int ks = 0; ks < NT / 2; ++ks) {
-        uint32_t pa[MT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          pa[mt][0] = pack2<E>(s[mt][2 * ks][0], s[mt][2 * ks][1]);
-          pa[mt][1] = pack2<E>(s[mt][2 * ks][2], s[mt][2 * ks][3]);
-          pa[mt][2] = pack2<E>(s[mt][2 * ks + 1][0], s[mt][2 * ks + 1][1]);
-          pa[mt][3] = pack2<E>(s[mt][2 * ks + 1][2], s[mt][2 * ks + 1][3]);
-        }
-#pragma unroll
-        for (int p = 0; p < DN / 2; ++p) {
-          uint32_t b[4];
-          ldmatrix4_trans(b, vt + (ks * 16 + vrow) * ROWB +
-                                 (((2 * p + (lane >> 4)) ^ (lane & 7)) << 4));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816<E>(o[mt][2 * p], pa[mt], b[0], b[1]);
-            mma16816<E>(o[mt][2 * p + 1], pa[mt], b[2], b[3]);
-          }
-        }
-      }
-    }
-    cp_async_wait<0>();
-    __syncthreads();   // every warp is done with its ring
-
-    // ---- join the warps: each leaves its rows' maximum, sum and output in shared memory
-    float* s_o = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int r = 0; r < 2 * MT; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      const int row = (lane >> 2) + 8 * r;
-      if ((lane & 3) == 0) s_ml[warp][row] = make_float2(m[r], l[r]);
-#pragma unroll
-      for (int x = 0; x < DN; ++x)
-        *reinterpret_cast<float2*>(s_o + (warp * RB + row) * OSTR + x * 8 + (lane & 3) * 2) =
-            make_float2(o[r >> 1][x][(r & 1) * 2], o[r >> 1][x][(r & 1) * 2 + 1]);
-    }
-    __syncthreads();
+    attend<E, D, MT, SEL>(a, en, hk, uo * UNIT, min(ntok, (uo + take) * UNIT), smem, s_ml);
     const bool whole = take == units;
     const int slot = 2 * cta + (uo == 0 ? 1 : 0);
     for (int i = tid; i < en.rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-      float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][r].x);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = s_ml[w][r];
-        const float f = ml.x == mm ? 1.f : exp2_approx(ml.x - base);
-        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * RB + r) * OSTR + c);
-        ll += ml.y * f;
-        acc.x += x.x * f;
-        acc.y += x.y * f;
-        acc.z += x.z * f;
-        acc.w += x.w * f;
-      }
+      float mm, ll;
+      const float4 acc = warp_sum<D, MT>(smem, s_ml, r, c, mm, ll);
       if (whole) {
-        const int rr = en.row0 + r, t = rr / a.G, g = rr - t * a.G;
-        const int64_t head = ((int64_t)en.n * a.T + t) * a.Hq + hk * a.G + g;
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        uint2 y;
-        y.x = pack2<E>(acc.x * inv, acc.y * inv);
-        y.y = pack2<E>(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<E*>(a.out) + head * D + c) = y;
-        if (a.lse && c == 0) a.lse[head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+        finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
       } else {
         *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c) = acc;
         if (c == 0) a.part_ml[slot * RB + r] = make_float2(mm, ll);
       }
     }
+    __syncthreads();   // the buffers are free for the next segment
     if (!whole && uo == 0) {
       // the CTA that holds the item's last unit x is floor(((x + 1) nc - 1) / total)
-      const long long end = u + units;
-      split = make_int2(e * a.Hkv + hk, (int)((end * nc - 1) / total));
+      split = make_int2(e * a.Hkv + hk, (int)(((u + units) * nc - 1) / total));
     }
     u += take;
     off += take;
@@ -506,49 +609,69 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const AttnArgs a) {
   float mm = a.part_ml[(2 * cta + 1) * RB + r].x;
 #pragma unroll 8
   for (int p = cta + 1; p <= sp.y; ++p) mm = fmaxf(mm, a.part_ml[2 * p * RB + r].x);
-  const float base = mm == -INFINITY ? 0.f : mm;
   float ll = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int p = cta; p <= sp.y; ++p) {
     const int slot = p == cta ? 2 * p + 1 : 2 * p;
     const float2 ml = a.part_ml[slot * RB + r];
-    const float4 x = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c);
-    const float f = ml.x == mm ? 1.f : exp2_approx(ml.x - base);
-    ll += ml.y * f;
-    acc.x += x.x * f;
-    acc.y += x.y * f;
-    acc.z += x.z * f;
-    acc.w += x.w * f;
+    add_part(acc, ll, mm, ml.x, ml.y,
+             *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c));
   }
-  const int rr = en.row0 + r, t = rr / a.G, g = rr - t * a.G;
-  const int64_t head = ((int64_t)en.n * a.T + t) * a.Hq + hk * a.G + g;
-  const float inv = ll == 0.f ? 0.f : 1.f / ll;
-  uint2 y;
-  y.x = pack2<E>(acc.x * inv, acc.y * inv);
-  y.y = pack2<E>(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<E*>(a.out) + head * D + c) = y;
-  if (a.lse && c == 0) a.lse[head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+  finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
 }
 
 int rows_per_item(const PagedAttn& p) { return p.topk > 0 ? p.Hq / p.Hkv : p.T * (p.Hq / p.Hkv); }
 
+// CTAs that share an item: 0 for equal ranges.
+int cluster_size(const PagedAttn& p) {
+  const int rows = rows_per_item(p), rb = rows > 16 ? 32 : 16, unit = kWarps * (2048 / p.d);
+  const int64_t items =
+      (int64_t)p.nseq * (p.topk > 0 ? p.T : 1) * ((rows + rb - 1) / rb) * p.Hkv;
+  const int64_t span = p.topk > 0 ? p.topk : (int64_t)p.max_pages * p.page_size;
+  const int64_t units = (span + unit - 1) / unit;   // of the longest item there can be
+  if (items > kMaxCtas) return 0;
+  int64_t c = (2 * items > kClusterCtas ? kMaxCtas : kClusterCtas) / items;
+  if (c > kMaxCluster) c = kMaxCluster;
+  if (c > units) c = units;
+  return (units + c - 1) / c <= kClusterUnits ? (int)c : 0;
+}
+
 template <typename E, int D, int MT, bool SEL>
 cudaError_t launch_variant(const PagedAttn& p, AttnArgs a, cudaStream_t st) {
-  constexpr int RB = 16 * MT, UNIT = kWarps * (2048 / D);
-  const int smem = kWarps * kStages * 2 * 4096 + RB * D * 2;
-  cudaError_t err = cudaFuncSetAttribute(paged_attn_kernel<E, D, MT, SEL>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (err != cudaSuccess) return err;
+  using S = Shape<D, MT>;
   const int rows = rows_per_item(p);
-  a.nb = (rows + RB - 1) / RB;
+  a.nb = (rows + S::RB - 1) / S::RB;
   const int64_t items = (int64_t)p.nseq * (SEL ? p.T : 1) * a.nb * p.Hkv;
+  const int size = cluster_size(p);
+  const auto kernel =
+      size ? paged_attn_cluster_kernel<E, D, MT, SEL> : paged_attn_kernel<E, D, MT, SEL>;
+  cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  if (err != cudaSuccess) return err;
+  if (size) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+  }
   const int64_t span = SEL ? p.topk : (int64_t)p.max_pages * p.page_size;
-  const int64_t units = (span + UNIT - 1) / UNIT;   // of the longest item there can be
+  const int64_t units = (span + S::UNIT - 1) / S::UNIT;   // of the longest item there can be
   const int grid = (int)(items * units < kMaxCtas ? items * units : kMaxCtas);
-  err = launch_pdl(paged_attn_kernel<E, D, MT, SEL>, dim3(grid), dim3(kThreads), smem, st, a);
+  err = launch_pdl(kernel, dim3(grid), dim3(kThreads), S::SMEM, st, a);
   if (err != cudaSuccess || units == 1) return err;
-  const int most = rows < RB ? rows : RB;
+  const int most = rows < S::RB ? rows : S::RB;
   constexpr int R = 128 / (D / 4);
   return launch_pdl(paged_join_kernel<E, D, MT, SEL>, dim3(grid, (most + R - 1) / R), dim3(128), 0,
                     st, a);
@@ -565,6 +688,7 @@ cudaError_t launch_type(const PagedAttn& p, const AttnArgs& a, cudaStream_t st) 
 }  // namespace
 
 size_t paged_attn_ws_bytes(const PagedAttn& p) {
+  if (cluster_size(p)) return 0;
   const size_t rb = rows_per_item(p) > 16 ? 32 : 16;
   return align256(2 * kMaxCtas * rb * p.d * sizeof(float)) +
          align256(2 * kMaxCtas * rb * sizeof(float2)) + align256(kMaxCtas * sizeof(int2));
@@ -597,7 +721,10 @@ cudaError_t launch_paged_attn(const PagedAttn& p, void* scratch, int* status, cu
   a.page_size = p.page_size;
   a.max_pages = p.max_pages;
   a.topk = p.topk;
-  a.scale2 = p.scale * kLog2e;
+  a.scale2 = p.scale == 0.f ? 1.f : std::fabs(p.scale) * kLog2e;
+  a.q_flip = p.scale < 0.f ? 0x80008000u : 0u;
+  a.q_keep = p.scale == 0.f ? 0u : 0xffffffffu;
+  a.by_page = Divide::by(p.page_size);
   if (p.dtype == MISA_DTYPE_BF16)
     return p.d == 128 ? launch_type<__nv_bfloat16, 128>(p, a, st)
                       : launch_type<__nv_bfloat16, 64>(p, a, st);

@@ -11,6 +11,8 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <climits>
+
 #include "internal.h"
 #include "misa.h"
 #include "paged.cuh"
@@ -19,11 +21,16 @@ namespace misa {
 namespace {
 
 namespace cg = cooperative_groups;
+using paged::Divide;
 
 constexpr int kPlanCtas = 8;       // the largest portable cluster
 constexpr int kPlanThreads = 1024;
 constexpr int kApplyThreads = 256;
 constexpr int kCopyUnroll = 4;
+constexpr int kForkUnroll = 4;
+// Tables that one cluster rewrites: larger ones want every SM.
+constexpr int kSmallEntries = kPlanCtas * kPlanThreads * kForkUnroll;
+constexpr int kSmallPages = 1 << 17;
 constexpr int kCopyBytes = kApplyThreads * 16 * kCopyUnroll;   // piece of a page that a block copies
 
 // Scratch of resize and compact (256-aligned regions).
@@ -100,73 +107,206 @@ struct Span {
   }
 };
 
-// Number of CTA-slice pages that are free (FREE) or live, summed over the block.
+// A slice's pages in tiles of kTile: bit p of the tile's words says whether the page is live
+// (refs > 0).  Pages behind the slice count as live (FREE) or free, so that no list takes them.
+constexpr int kTile = kPlanThreads * 32;
+
 template <bool FREE>
-__device__ __forceinline__ int count_slice(const int32_t* __restrict__ refs, int lo, int hi,
-                                           int* s_scan) {
+__device__ __forceinline__ void load_bits(const int32_t* refs, int lo, int hi, int32_t* out_refs,
+                                          uint32_t* s_bits) {
+  const int lane = threadIdx.x & 31;
+  const int words = (min(hi - lo, kTile) + 31) / 32;
+#pragma unroll 4
+  for (int w = threadIdx.x >> 5; w < words; w += kPlanThreads / 32) {
+    const int p = lo + w * 32 + lane;
+    const int r = p < hi ? refs[p] : FREE;
+    if (out_refs != refs && p < hi) out_refs[p] = r;
+    const uint32_t live = __ballot_sync(0xffffffffu, r > 0);
+    if (lane == 0) s_bits[w] = live;
+  }
+  if ((int)threadIdx.x >= words) s_bits[threadIdx.x] = FREE ? 0xffffffffu : 0u;
+  __syncthreads();
+}
+
+// Pages of the slice that are free (FREE) or live.  out_refs receives the counts where it is
+// another buffer; the last tile's bits stay in s_bits.
+template <bool FREE>
+__device__ __forceinline__ int count_slice(const int32_t* refs, int lo, int hi, int32_t* out_refs,
+                                           uint32_t* s_bits, int* s_scan) {
   int n = 0;
-  for (int p = lo + threadIdx.x; p < hi; p += kPlanThreads) n += (refs[p] > 0) != FREE;
+  for (int t = lo; t < hi; t += kTile) {
+    load_bits<FREE>(refs, t, hi, out_refs, s_bits);
+    n += __popc(FREE ? ~s_bits[threadIdx.x] : s_bits[threadIdx.x]);
+    __syncthreads();
+  }
   int total;
   block_scan(n, s_scan, &total);
   return total;
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
-    resize_plan_kernel(const int32_t* __restrict__ table, const int32_t* refs,
-                       const int32_t* __restrict__ old_len, const int32_t* __restrict__ new_len,
-                       int nseq, int max_pages, int num_pages, int page_size, int32_t* out_refs,
-                       PlanScratch s, int* status) {
+// Calls f(page, is it free (FREE) or live, rank) for every page of the slice, ranks counted from
+// `before`, until they reach `stop`; a warp's lanes have 32 neighbouring pages.
+template <bool FREE, typename F>
+__device__ __forceinline__ void rank_slice(const int32_t* refs, int lo, int hi, int before,
+                                           int stop, uint32_t* s_bits, int* s_at, int* s_scan,
+                                           F f) {
+  const int lane = threadIdx.x & 31;
+  for (int t = lo; t < hi && before < stop; t += kTile) {
+    if (hi - lo > kTile) load_bits<FREE>(refs, t, hi, const_cast<int32_t*>(refs), s_bits);
+    int n;
+    const uint32_t mine = FREE ? ~s_bits[threadIdx.x] : s_bits[threadIdx.x];
+    s_at[threadIdx.x] = before + block_scan(__popc(mine), s_scan, &n);
+    __syncthreads();
+    const int words = (min(hi - t, kTile) + 31) / 32;
+    for (int w = threadIdx.x >> 5; w < words; w += kPlanThreads / 32) {
+      const uint32_t bits = FREE ? ~s_bits[w] : s_bits[w];
+      const int p = t + w * 32 + lane;
+      if (p < hi) f(p, (bits >> lane) & 1u, s_at[w] + __popc(bits & ((1u << lane) - 1u)));
+    }
+    __syncthreads();
+    before += n;
+  }
+}
+
+// What the calls of one resize share.
+struct ResizeArgs {
+  const int32_t* table;
+  const int32_t* refs;
+  const int32_t* old_len;
+  const int32_t* new_len;
+  int32_t* out_table;
+  int32_t* out_refs;
+  int* status;
+  int nseq, max_pages, num_pages, page_size;
+  Divide by_row;   // division by max_pages
+  PlanScratch s;
+};
+
+// The table's entries from `first` on, `step` apart, and the counts of the pages they let go of
+// and take.  kForkUnroll entries at a time, whose lookups are in flight together.
+__device__ __forceinline__ void resize_entries(const ResizeArgs& a, bool go, int first, int step) {
+  const int entries = a.nseq * a.max_pages;
+  for (int64_t i0 = first; i0 < entries; i0 += (int64_t)step * kForkUnroll) {
+    int was[kForkUnroll], o[kForkUnroll], x[kForkUnroll], cow[kForkUnroll], at[kForkUnroll],
+        col[kForkUnroll];
+#pragma unroll
+    for (int u = 0; u < kForkUnroll; ++u) {
+      const int64_t i = i0 + (int64_t)u * step;
+      if (i >= entries) break;
+      const int n = a.by_row((int)i);
+      col[u] = (int)i - n * a.max_pages;
+      was[u] = a.table[i];
+      o[u] = a.old_len[n];
+      x[u] = a.new_len[n];
+      cow[u] = a.s.cow[n];
+      at[u] = a.s.first[n];
+    }
+#pragma unroll
+    for (int u = 0; u < kForkUnroll; ++u) {
+      const int64_t i = i0 + (int64_t)u * step;
+      if (i >= entries) break;
+      const Span sp(o[u], x[u], a.page_size, a.max_pages);
+      int now = was[u];
+      if (go && sp.ok) {
+        const int c = col[u];
+        const bool copy = cow[u] >= 0;
+        if (c >= max(sp.oldp, sp.newp)) {
+          now = -1;
+        } else if (c >= sp.oldp) {
+          now = a.s.list[at[u] + copy + (c - sp.oldp)];
+          a.out_refs[now] = 1;
+        } else if (c >= sp.newp || (copy && c == sp.tail)) {
+          if ((unsigned)was[u] < (unsigned)a.num_pages)
+            atomicSub(a.out_refs + was[u], 1);
+          else
+            set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
+          now = -1;
+          if (c < sp.newp) {
+            now = a.s.list[at[u]];
+            a.out_refs[now] = 1;
+          }
+        }
+      }
+      if (now != was[u] || a.out_table != a.table) a.out_table[i] = now;
+    }
+  }
+}
+
+// APPLY: the cluster rewrites the table too (a small table, no pools), so that one launch does it.
+template <bool APPLY>
+__global__ void __launch_bounds__(kPlanThreads, 1) resize_plan_kernel(const ResizeArgs a) {
   __shared__ int s_scan[32];
+  __shared__ uint32_t s_bits[kPlanThreads];
+  __shared__ int s_at[kPlanThreads];
   __shared__ int s_free, s_need;
   pdl_prologue();
   cg::cluster_group cluster = cg::this_cluster();
+  const PlanScratch& s = a.s;
   const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
-  const int slice = (num_pages + kPlanCtas - 1) / kPlanCtas;
-  const int lo = min(num_pages, rank * slice), hi = min(num_pages, lo + slice);
-  const int n_free = count_slice<true>(refs, lo, hi, s_scan);
-  if (tid == 0) s_free = n_free;
-
-  if (rank == 0) {
-    // pages whose last token's sequence grows: how many such sequences hold it, and the last
-    auto tail_page = [&](int n, const Span& sp) {
-      if (sp.tail < 0) return -1;
-      const int p = table[(int64_t)n * max_pages + sp.tail];
-      return (unsigned)p < (unsigned)num_pages ? p : -1;
+  // CTA 0 sees what the sequences want while the others count the free pages of their slices
+  const int slice = (a.num_pages + kPlanCtas - 2) / (kPlanCtas - 1);
+  const int lo = rank == 0 ? 0 : min(a.num_pages, (rank - 1) * slice);
+  const int hi = rank == 0 ? 0 : min(a.num_pages, lo + slice);
+  if (rank > 0) {
+    const int n_free = count_slice<true>(a.refs, lo, hi, a.out_refs, s_bits, s_scan);
+    if (tid == 0) s_free = n_free;
+  } else {
+    if (tid == 0) s_free = 0;
+    // what sequence n wants: `want` pages, without the copy of a last page that others hold;
+    // that page (-1: none)
+    auto look = [&](int n, int& want, int& page) {
+      want = 0;
+      page = -1;
+      if (n >= a.nseq) return;
+      const Span sp(a.old_len[n], a.new_len[n], a.page_size, a.max_pages);
+      want = max(0, sp.newp - sp.oldp);
+      if (!sp.ok) set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
+      if (sp.tail < 0) return;
+      const int p = a.table[(int64_t)n * a.max_pages + sp.tail];
+      if ((unsigned)p >= (unsigned)a.num_pages)
+        set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
+      else if (a.refs[p] > 1)
+        page = p;
     };
-    for (int n = tid; n < nseq; n += kPlanThreads) {
-      const int p = tail_page(n, Span(old_len[n], new_len[n], page_size, max_pages));
-      if (p >= 0) {
-        s.list2[p] = 0;
-        s.map[p] = -1;
+    int want, page;
+    bool any = false;
+    for (int n = tid; n < a.nseq; n += kPlanThreads) {
+      look(n, want, page);
+      if (page >= 0) {
+        any = true;
+        s.list2[page] = 0;
+        s.map[page] = -1;
       }
     }
-    __syncthreads();
-    for (int n = tid; n < nseq; n += kPlanThreads) {
-      const int p = tail_page(n, Span(old_len[n], new_len[n], page_size, max_pages));
-      if (p >= 0) {
-        atomicAdd(s.list2 + p, 1);
-        atomicMax(s.map + p, n);
-      }
+    const bool one = a.nseq <= kPlanThreads;   // what look() said is still at hand
+    if (tid >= a.nseq) {
+      want = 0;
+      page = -1;
     }
-    __syncthreads();
-    int need = 0, copies = 0;
-    for (int n0 = 0; n0 < nseq; n0 += kPlanThreads) {
-      const int n = n0 + tid;
-      int want = 0, page = -1;
-      if (n < nseq) {
-        const Span sp(old_len[n], new_len[n], page_size, max_pages);
-        const int p = tail_page(n, sp);
-        if (!sp.ok || (sp.tail >= 0 && p < 0)) set_status(status, MISA_ERR_BAD_DEVICE_INPUT);
-        if (p >= 0) {
-          const int holders = refs[p];
-          if (holders > 1 && !(__ldcg(s.list2 + p) >= holders && __ldcg(s.map + p) == n)) page = p;
+    if (__syncthreads_or(any)) {   // how many of its holders grow, and the last of them
+      for (int n = tid; n < a.nseq; n += kPlanThreads) {
+        if (!one) look(n, want, page);
+        if (page >= 0) {
+          atomicAdd(s.list2 + page, 1);
+          atomicMax(s.map + page, n);
         }
-        want = max(0, sp.newp - sp.oldp) + (page >= 0);
       }
-      int sum, ncow;
+      __syncthreads();
+    }
+    int need = 0, copies = 0;
+    for (int n0 = 0; n0 < a.nseq; n0 += kPlanThreads) {
+      const int n = n0 + tid;
+      if (!one) look(n, want, page);
+      if (page >= 0) {
+        if (__ldcg(s.list2 + page) >= a.refs[page] && __ldcg(s.map + page) == n)
+          page = -1;   // the last of its holders, who all grow, keeps it
+        else
+          ++want;
+      }
+      int sum, ncow = 0, at = 0;
       const int before = block_scan(want, s_scan, &sum);
-      const int at = block_scan(page >= 0, s_scan, &ncow);
-      if (n < nseq) {
+      if (__syncthreads_or(page >= 0)) at = block_scan(page >= 0, s_scan, &ncow);
+      if (n < a.nseq) {
         s.first[n] = need + before;
         s.cow[n] = page;
         if (page >= 0) s.cow_seq[copies + at] = n;
@@ -182,6 +322,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   cluster.sync();
   const int need = *cluster.map_shared_rank(&s_need, 0);
   int before = 0, total = 0;
+#pragma unroll
   for (int r = 0; r < kPlanCtas; ++r) {
     const int f = *cluster.map_shared_rank(&s_free, r);
     if (r < rank) before += f;
@@ -190,101 +331,91 @@ __global__ void __launch_bounds__(kPlanThreads)
   const bool go = need <= total;
   if (rank == 0 && tid == 0) {
     s.head[2] = go;
-    if (!go) set_status(status, MISA_ERR_OUT_OF_PAGES);
+    if (!go) set_status(a.status, MISA_ERR_OUT_OF_PAGES);
   }
-  const bool copy_refs = out_refs != refs;
-  for (int p0 = lo; p0 < hi && (copy_refs || (go && before < need)); p0 += kPlanThreads) {
-    const int p = p0 + tid;
-    const int r = p < hi ? refs[p] : 1;
-    if (copy_refs && p < hi) out_refs[p] = r;
-    int n;
-    const int at = before + block_scan(r <= 0, s_scan, &n);
-    if (go && r <= 0 && at < need) s.list[at] = p;
-    before += n;
+  if (go)
+    rank_slice<true>(a.refs, lo, hi, before, need, s_bits, s_at, s_scan,
+                     [&](int p, bool free, int at) {
+                       if (free && at < need) s.list[at] = p;
+                     });
+  cluster.sync();   // the list is complete, and no CTA reads another's shared memory any more
+  if constexpr (APPLY) {
+    resize_entries(a, go, rank * kPlanThreads + tid, kPlanCtas * kPlanThreads);
   }
-  cluster.sync();   // no CTA leaves while another reads its shared memory
 }
 
-// One piece of a page, by the whole block.  src and dst: pages.
-__device__ __forceinline__ void copy_piece(const PagePools& pools, int pool, int src, int dst,
-                                           int piece) {
-  const uint32_t bytes = pools.page_bytes[pool];
-  const uint32_t at = (uint32_t)piece * kCopyBytes;
-  if (at >= bytes) return;
-  const uint4* from =
-      reinterpret_cast<const uint4*>(pools.base[pool] + (size_t)src * bytes + at) + threadIdx.x;
-  uint4* to = reinterpret_cast<uint4*>(pools.base[pool] + (size_t)dst * bytes + at) + threadIdx.x;
-  const int n = (int)(min(bytes - at, (uint32_t)kCopyBytes) / 16) - (int)threadIdx.x;
-  uint4 x[kCopyUnroll];
+// Copies of pages, a piece (kCopyBytes of one page in one pool) per block and step; page_of(m,
+// &src, &dst) tells copy m's pages.  The next piece's loads are in flight while one is stored.
+template <typename F>
+__device__ __forceinline__ void copy_pages(const PagePools& pools, int pieces, int copies,
+                                           F page_of) {
+  const int64_t per = (int64_t)pools.n * pieces, work = copies * per;
+  uint4 x[2][kCopyUnroll];
+  uint4* to[2];
+  int left[2];   // 16-byte words from this thread's first one to the piece's end
+  auto load = [&](int64_t i, int b) {
+    left[b] = 0;
+    if (i >= work) return;
+    const int m = (int)(i / per), y = (int)(i - m * per), pool = y / pieces;
+    const uint32_t bytes = pools.page_bytes[pool], at = (uint32_t)(y - pool * pieces) * kCopyBytes;
+    if (at >= bytes) return;
+    int src, dst;
+    page_of(m, &src, &dst);
+    unsigned char* base = pools.base[pool] + at;
+    const uint4* from = reinterpret_cast<const uint4*>(base + (size_t)src * bytes) + threadIdx.x;
+    to[b] = reinterpret_cast<uint4*>(base + (size_t)dst * bytes) + threadIdx.x;
+    left[b] = (int)(min(bytes - at, (uint32_t)kCopyBytes) / 16) - (int)threadIdx.x;
 #pragma unroll
-  for (int u = 0; u < kCopyUnroll; ++u)
-    if (u * kApplyThreads < n) x[u] = __ldcs(from + u * kApplyThreads);
+    for (int u = 0; u < kCopyUnroll; ++u)
+      if (u * kApplyThreads < left[b]) x[b][u] = __ldcs(from + u * kApplyThreads);
+  };
+  auto store = [&](int b) {
 #pragma unroll
-  for (int u = 0; u < kCopyUnroll; ++u)
-    if (u * kApplyThreads < n) to[u * kApplyThreads] = x[u];
+    for (int u = 0; u < kCopyUnroll; ++u)
+      if (u * kApplyThreads < left[b]) __stcs(to[b] + u * kApplyThreads, x[b][u]);
+  };
+  load(blockIdx.x, 0);
+  for (int64_t i = blockIdx.x; i < work; i += 2 * (int64_t)gridDim.x) {
+    load(i + gridDim.x, 1);
+    store(0);
+    load(i + 2 * (int64_t)gridDim.x, 0);
+    store(1);
+  }
 }
 
-__global__ void __launch_bounds__(kApplyThreads)
-    resize_apply_kernel(const int32_t* table, const int32_t* __restrict__ old_len,
-                        const int32_t* __restrict__ new_len, int nseq, int max_pages,
-                        int num_pages, int page_size, const __grid_constant__ PagePools pools,
-                        int pieces, int32_t* out_table, int32_t* out_refs, PlanScratch s,
-                        int* status) {
+__global__ void __launch_bounds__(kApplyThreads, 4)
+    resize_apply_kernel(const ResizeArgs a, const __grid_constant__ PagePools pools, int pieces) {
   pdl_prologue();
-  const bool go = s.head[2] != 0;
-  const int64_t entries = (int64_t)nseq * max_pages;
-  for (int64_t i = (int64_t)blockIdx.x * kApplyThreads + threadIdx.x; i < entries;
-       i += (int64_t)gridDim.x * kApplyThreads) {
-    const int n = (int)(i / max_pages), c = (int)(i - (int64_t)n * max_pages);
-    const int was = table[i];
-    const Span sp(old_len[n], new_len[n], page_size, max_pages);
-    int now = was;
-    if (go && sp.ok) {
-      const int page = s.cow[n];
-      if (c >= max(sp.oldp, sp.newp)) {
-        now = -1;
-      } else if (c >= sp.oldp) {
-        now = s.list[s.first[n] + (page >= 0) + (c - sp.oldp)];
-        out_refs[now] = 1;
-      } else if (c >= sp.newp || (page >= 0 && c == sp.tail)) {
-        if ((unsigned)was < (unsigned)num_pages)
-          atomicSub(out_refs + was, 1);
-        else
-          set_status(status, MISA_ERR_BAD_DEVICE_INPUT);
-        now = -1;
-        if (c < sp.newp) {
-          now = s.list[s.first[n]];
-          out_refs[now] = 1;
-        }
-      }
-    }
-    if (now != was || out_table != table) out_table[i] = now;
-  }
-  if (!go || pools.n == 0) return;
-  const int64_t per = (int64_t)pools.n * pieces, work = s.head[0] * per;
-  for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-    const int n = s.cow_seq[i / per], x = (int)(i % per);
-    copy_piece(pools, x / pieces, s.cow[n], s.list[s.first[n]], x % pieces);
-  }
+  const bool go = a.s.head[2] != 0;
+  resize_entries(a, go, blockIdx.x * kApplyThreads + threadIdx.x, gridDim.x * kApplyThreads);
+  if (go && pools.n > 0)
+    copy_pages(pools, pieces, a.s.head[0], [&](int m, int* src, int* dst) {
+      const int n = a.s.cow_seq[m];
+      *src = a.s.cow[n];
+      *dst = a.s.list[a.s.first[n]];
+    });
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
     compact_plan_kernel(const int32_t* refs, int num_pages, int32_t* out_refs, int32_t* n_live_out,
                         PlanScratch s) {
   __shared__ int s_scan[32];
+  __shared__ uint32_t s_bits[kPlanThreads];
+  __shared__ int s_at[kPlanThreads];
   __shared__ int s_live, s_holes;
   pdl_prologue();
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
   const int slice = (num_pages + kPlanCtas - 1) / kPlanCtas;
   const int lo = min(num_pages, rank * slice), hi = min(num_pages, lo + slice);
-  const int live = count_slice<false>(refs, lo, hi, s_scan);
+  const int live = count_slice<false>(refs, lo, hi, out_refs, s_bits, s_scan);
   if (tid == 0) {
     s_live = live;
     s_holes = 0;
   }
   cluster.sync();
   int before = 0, n_live = 0;
+#pragma unroll
   for (int r = 0; r < kPlanCtas; ++r) {
     const int f = *cluster.map_shared_rank(&s_live, r);
     if (r < rank) before += f;
@@ -292,29 +423,24 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   // hole i below n_live goes to list[i]; the live page of rank i from n_live on to list2[i]
   int holes = 0;
-  for (int p0 = lo; p0 < hi; p0 += kPlanThreads) {
-    const int p = p0 + tid;
-    const int r = p < hi ? refs[p] : 0;
-    int n;
-    const int at = before + block_scan(r > 0, s_scan, &n);
-    before += n;
-    if (p < hi) {
-      if (out_refs != refs) out_refs[p] = r;
-      if (p < n_live && r <= 0) {
-        s.list[p - at] = p;
-        ++holes;
-      }
-      if (p >= n_live) {
-        if (r > 0) s.list2[at] = p;
-        s.map[p] = -1;
-      }
-    }
-  }
+  rank_slice<false>(refs, lo, hi, before, INT_MAX, s_bits, s_at, s_scan,
+                    [&](int p, bool is_live, int at) {
+                      if (p < n_live) {
+                        if (!is_live) {
+                          s.list[p - at] = p;
+                          ++holes;
+                        }
+                      } else {
+                        if (is_live) s.list2[at] = p;
+                        s.map[p] = -1;
+                      }
+                    });
   int sum;
   block_scan(holes, s_scan, &sum);
   if (tid == 0) s_holes = sum;
   cluster.sync();
   int moves = 0;
+#pragma unroll
   for (int r = 0; r < kPlanCtas; ++r) moves += *cluster.map_shared_rank(&s_holes, r);
   for (int i = rank * kPlanThreads + tid; i < moves; i += kPlanCtas * kPlanThreads) {
     const int src = __ldcg(s.list2 + n_live - moves + i), dst = __ldcg(s.list + i);
@@ -330,14 +456,14 @@ __global__ void __launch_bounds__(kPlanThreads)
   cluster.sync();
 }
 
-__global__ void __launch_bounds__(kApplyThreads)
-    compact_apply_kernel(const int32_t* table, int64_t entries, int num_pages,
+__global__ void __launch_bounds__(kApplyThreads, 4)
+    compact_apply_kernel(const int32_t* table, int entries, int num_pages,
                          const __grid_constant__ PagePools pools, int pieces, int32_t* out_table,
                          PlanScratch s, int* status) {
   pdl_prologue();
   const int moves = s.head[0], n_live = s.head[1];
-  for (int64_t i = (int64_t)blockIdx.x * kApplyThreads + threadIdx.x; i < entries;
-       i += (int64_t)gridDim.x * kApplyThreads) {
+  for (int i = blockIdx.x * kApplyThreads + threadIdx.x; i < entries;
+       i += gridDim.x * kApplyThreads) {
     const int was = table[i];
     int now = was;
     if (was < -1 || was >= num_pages) {
@@ -351,39 +477,87 @@ __global__ void __launch_bounds__(kApplyThreads)
     }
     if (now != was || out_table != table) out_table[i] = now;
   }
-  if (pools.n == 0) return;
-  const int64_t per = (int64_t)pools.n * pieces, work = moves * per;
-  for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-    const int m = (int)(i / per), x = (int)(i % per);
-    copy_piece(pools, x / pieces, s.list2[n_live - moves + m], s.list[m], x % pieces);
+  if (pools.n > 0)
+    copy_pages(pools, pieces, moves, [&](int m, int* src, int* dst) {
+      *src = s.list2[n_live - moves + m];
+      *dst = s.list[m];
+    });
+}
+
+struct ForkArgs {
+  const int32_t* table;
+  const int32_t* parent;
+  int32_t* out_table;
+  int32_t* out_refs;
+  int* status;
+  int nseq, max_pages, num_pages, entries;
+  Divide by_row;   // division by max_pages
+};
+
+// Entry i = n * max_pages + c before and after: row n takes the entries of row parent[n].
+__device__ __forceinline__ void fork_read(const ForkArgs& a, int i, int& was, int& now) {
+  const int n = a.by_row(i);
+  int from = a.parent[n];
+  if (from < -1 || from >= a.nseq) {
+    set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
+    from = n;
+  }
+  was = a.table[i];
+  now = from < 0 ? -1 : a.table[i + (from - n) * a.max_pages];
+}
+
+// The counts follow; an entry that stays the same touches none.
+__device__ __forceinline__ void fork_write(const ForkArgs& a, int i, int was, int now) {
+  if (was < -1 || was >= a.num_pages) set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
+  if (now != was) {
+    if ((unsigned)now < (unsigned)a.num_pages) atomicAdd(a.out_refs + now, 1);
+    if ((unsigned)was < (unsigned)a.num_pages) atomicSub(a.out_refs + was, 1);
+  }
+  if (now != was || a.out_table != a.table) a.out_table[i] = now;
+}
+
+// A table of at most kPlanCtas * kPlanThreads * kForkUnroll entries by one cluster: everything is
+// read (and refs copied) before anything is written, so that it also works in place.
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    fork_small_kernel(const ForkArgs a, const int32_t* refs) {
+  pdl_prologue();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int at = (int)cluster.block_rank() * kPlanThreads + threadIdx.x;
+  constexpr int kStep = kPlanCtas * kPlanThreads;
+  int was[kForkUnroll], now[kForkUnroll];
+#pragma unroll
+  for (int u = 0; u < kForkUnroll; ++u)
+    if (at + u * kStep < a.entries) fork_read(a, at + u * kStep, was[u], now[u]);
+  if (a.out_refs != refs)
+    for (int p = at; p < a.num_pages; p += kStep) a.out_refs[p] = refs[p];
+  cluster.sync();
+#pragma unroll
+  for (int u = 0; u < kForkUnroll; ++u)
+    if (at + u * kStep < a.entries) fork_write(a, at + u * kStep, was[u], now[u]);
+}
+
+__global__ void __launch_bounds__(kApplyThreads) fork_kernel(const ForkArgs a) {
+  pdl_prologue();
+  const int step = gridDim.x * kApplyThreads;
+  for (int64_t i0 = blockIdx.x * kApplyThreads + threadIdx.x; i0 < a.entries;
+       i0 += (int64_t)step * kForkUnroll) {
+    int was[kForkUnroll], now[kForkUnroll];
+#pragma unroll
+    for (int u = 0; u < kForkUnroll; ++u)
+      if (i0 + (int64_t)u * step < a.entries) fork_read(a, (int)(i0 + u * step), was[u], now[u]);
+#pragma unroll
+    for (int u = 0; u < kForkUnroll; ++u)
+      if (i0 + (int64_t)u * step < a.entries) fork_write(a, (int)(i0 + u * step), was[u], now[u]);
   }
 }
 
-// Row n takes the entries of row parent[n] of `table`; the counts of the pages it lets go of and
-// takes follow (entries that stay the same touch no count).  out_refs holds the counts before.
+// 32-bit words from one buffer to another, neither overlapping the other.
 __global__ void __launch_bounds__(kApplyThreads)
-    fork_kernel(const int32_t* __restrict__ table, const int32_t* __restrict__ parent, int nseq,
-                int max_pages, int num_pages, int32_t* __restrict__ out_table, int32_t* out_refs,
-                int* status) {
+    copy_words_kernel(const int32_t* __restrict__ from, int32_t* __restrict__ to, int n) {
   pdl_prologue();
-  const int64_t entries = (int64_t)nseq * max_pages;
-  for (int64_t i = (int64_t)blockIdx.x * kApplyThreads + threadIdx.x; i < entries;
-       i += (int64_t)gridDim.x * kApplyThreads) {
-    const int n = (int)(i / max_pages), c = (int)(i - (int64_t)n * max_pages);
-    int from = parent[n];
-    if (from < -1 || from >= nseq) {
-      set_status(status, MISA_ERR_BAD_DEVICE_INPUT);
-      from = n;
-    }
-    const int was = table[i];
-    const int now = from < 0 ? -1 : table[(int64_t)from * max_pages + c];
-    if (was < -1 || was >= num_pages) set_status(status, MISA_ERR_BAD_DEVICE_INPUT);
-    if (now != was) {
-      if ((unsigned)now < (unsigned)num_pages) atomicAdd(out_refs + now, 1);
-      if ((unsigned)was < (unsigned)num_pages) atomicSub(out_refs + was, 1);
-    }
-    out_table[i] = now;
-  }
+  for (int64_t i = blockIdx.x * kApplyThreads + threadIdx.x; i < n;
+       i += gridDim.x * kApplyThreads)
+    to[i] = from[i];
 }
 
 template <typename... KArgs, typename... Args>
@@ -415,9 +589,9 @@ int pieces_of(const PagePools& pools) {
 
 // Blocks of the wide kernels: the table's entries and at most `copies` page copies, eight blocks
 // per SM (148) at most.
-int apply_grid(int64_t entries, int64_t copies, const PagePools& pools, int pieces) {
+int apply_grid(int64_t entries, int64_t copies, const PagePools* pools, int pieces) {
   int64_t n = (entries + kApplyThreads - 1) / kApplyThreads;
-  const int64_t c = copies * pools.n * pieces;
+  const int64_t c = pools ? copies * pools->n * pieces : 0;
   if (c > n) n = c;
   return (int)(n < 148 * 8 ? n : 148 * 8);
 }
@@ -426,42 +600,48 @@ int apply_grid(int64_t entries, int64_t copies, const PagePools& pools, int piec
 
 size_t pages_ws_bytes(int nseq, int num_pages) { return plan_scratch(nseq, num_pages, nullptr, nullptr); }
 
+// A large table that changes in place is read from a copy.
+size_t fork_ws_bytes(int nseq, int max_pages, int num_pages) {
+  const int64_t entries = (int64_t)nseq * max_pages;
+  return entries <= kSmallEntries && num_pages <= kSmallPages ? 0 : align256(entries * 4);
+}
+
 cudaError_t launch_pages_resize(const int32_t* table, const int32_t* refs, const int32_t* old_len,
                                 const int32_t* new_len, int nseq, int max_pages, int num_pages,
                                 int page_size, const PagePools& pools, int32_t* out_table,
                                 int32_t* out_refs, void* scratch, int* status, cudaStream_t st) {
-  PlanScratch s;
-  plan_scratch(nseq, num_pages, scratch, &s);
-  cudaError_t e = launch_plan(resize_plan_kernel, st, table, refs, old_len, new_len, nseq,
-                              max_pages, num_pages, page_size, out_refs, s, status);
+  ResizeArgs a = {table,  refs, old_len,   new_len,   out_table, out_refs,
+                  status, nseq, max_pages, num_pages, page_size, Divide::by(max_pages)};
+  plan_scratch(nseq, num_pages, scratch, &a.s);
+  const int entries = nseq * max_pages;
+  if (pools.n == 0 && entries <= kSmallEntries)
+    return launch_plan(resize_plan_kernel<true>, st, a);
+  const cudaError_t e = launch_plan(resize_plan_kernel<false>, st, a);
   if (e != cudaSuccess) return e;
   const int pieces = pieces_of(pools);
-  const int grid = apply_grid((int64_t)nseq * max_pages, nseq, pools, pieces);
-  return launch_pdl(resize_apply_kernel, dim3(grid), dim3(kApplyThreads), 0, st, table, old_len,
-                    new_len, nseq, max_pages, num_pages, page_size, pools, pieces, out_table,
-                    out_refs, s, status);
+  return launch_pdl(resize_apply_kernel, dim3(apply_grid(entries, nseq, &pools, pieces)),
+                    dim3(kApplyThreads), 0, st, a, pools, pieces);
 }
 
 cudaError_t launch_pages_fork(const int32_t* table, const int32_t* refs, const int32_t* parent,
                               int nseq, int max_pages, int num_pages, int32_t* out_table,
                               int32_t* out_refs, void* scratch, int* status, cudaStream_t st) {
-  const size_t table_bytes = (size_t)nseq * max_pages * sizeof(int32_t);
-  if (out_refs != refs) {
-    const cudaError_t e = cudaMemcpyAsync(out_refs, refs, (size_t)num_pages * sizeof(int32_t),
-                                          cudaMemcpyDeviceToDevice, st);
-    if (e != cudaSuccess) return e;
+  ForkArgs a = {table,     parent,    out_table,        out_refs,              status, nseq,
+                max_pages, num_pages, nseq * max_pages, Divide::by(max_pages)};
+  if (a.entries <= kSmallEntries && num_pages <= kSmallPages)
+    return launch_plan(fork_small_kernel, st, a, refs);
+  cudaError_t e = cudaSuccess;
+  if (out_refs != refs)
+    e = launch_pdl(copy_words_kernel, dim3(apply_grid(num_pages, 0, nullptr, 0)),
+                   dim3(kApplyThreads), 0, st, refs, out_refs, num_pages);
+  if (e == cudaSuccess && out_table == table) {   // rows read one another: in place, from a copy
+    e = launch_pdl(copy_words_kernel, dim3(apply_grid(a.entries, 0, nullptr, 0)),
+                   dim3(kApplyThreads), 0, st, table, static_cast<int32_t*>(scratch), a.entries);
+    a.table = static_cast<const int32_t*>(scratch);
   }
-  if (out_table == table) {   // rows read one another: in place they read a copy
-    const cudaError_t e =
-        cudaMemcpyAsync(scratch, table, table_bytes, cudaMemcpyDeviceToDevice, st);
-    if (e != cudaSuccess) return e;
-    table = static_cast<const int32_t*>(scratch);
-  }
-  const int64_t entries = (int64_t)nseq * max_pages;
-  const int64_t blocks = (entries + kApplyThreads - 1) / kApplyThreads;
-  return launch_pdl(fork_kernel, dim3((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8)),
-                    dim3(kApplyThreads), 0, st, table, parent, nseq, max_pages, num_pages,
-                    out_table, out_refs, status);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fork_kernel, dim3(apply_grid(a.entries, 0, nullptr, 0)), dim3(kApplyThreads),
+                    0, st, a);
 }
 
 cudaError_t launch_pages_compact(const int32_t* table, const int32_t* refs, int nseq,
@@ -473,10 +653,10 @@ cudaError_t launch_pages_compact(const int32_t* table, const int32_t* refs, int 
   cudaError_t e = launch_plan(compact_plan_kernel, st, refs, num_pages, out_refs, n_live, s);
   if (e != cudaSuccess) return e;
   const int pieces = pieces_of(pools);
-  const int64_t entries = (int64_t)nseq * max_pages;
-  const int grid = apply_grid(entries, num_pages / 2, pools, pieces);
-  return launch_pdl(compact_apply_kernel, dim3(grid), dim3(kApplyThreads), 0, st, table, entries,
-                    num_pages, pools, pieces, out_table, s, status);
+  const int entries = nseq * max_pages;
+  return launch_pdl(compact_apply_kernel, dim3(apply_grid(entries, num_pages / 2, &pools, pieces)),
+                    dim3(kApplyThreads), 0, st, table, entries, num_pages, pools, pieces,
+                    out_table, s, status);
 }
 
 }  // namespace misa

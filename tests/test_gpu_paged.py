@@ -352,13 +352,14 @@ def test_misaligned_and_short_buffers_are_refused(M):
         M.misa_paged_attention(odd, k, v, table, pos)
     assert e.value.status == 1
     from long_context_block_b200 import _binding as b
-    nb = b.library().misa_paged_attention_workspace_size(1, 1, 4, 2, 128, 0)
+    nb = b.library().misa_paged_attention_workspace_size(1, 1, 4, 2, 128, 16, 4096, 0)
     ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    wide = torch.full((1, 4096), -1, dtype=torch.int32, device="cuda")
     out = torch.empty_like(q)
     rc = b.library().misa_paged_attention(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), table.data_ptr(), pos.data_ptr(), None, 0, 1, 1,
-        4, 2, 128, k.shape[0], 16, table.shape[1], 0, 0.1, out.data_ptr(), None, None,
-        ws.data_ptr(), nb - 1, None)
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), wide.data_ptr(), pos.data_ptr(), None, 0, 1, 1,
+        4, 2, 128, k.shape[0], 16, 4096, 0, 0.1, out.data_ptr(), None, None, ws.data_ptr(), nb - 1,
+        None)
     assert rc == 5
 
 

@@ -18,22 +18,30 @@ def lib():
 def test_workspace_sizes(lib):
     c = lib.library()
     a256 = lambda x: (x + 255) // 256 * 256
-    # partials: two row blocks per CTA (296 at most), of 16 rows, or 32 when more share a head
+    # nseq, T, Hq, Hkv, d, page_size, max_pages, topk.  Partials: two row blocks per CTA (296 at
+    # most), of 16 rows, or 32 when more share a head
     att = lambda rb, d: a256(592 * rb * d * 4) + a256(592 * rb * 8) + a256(296 * 8)
     f = c.misa_paged_attention_workspace_size
-    assert f(32, 1, 32, 8, 128, 0) == att(16, 128)
-    assert f(32, 1, 32, 8, 64, 2048) == att(16, 64)
-    assert f(8, 16, 32, 8, 128, 0) == att(32, 128)
-    assert f(8, 16, 32, 8, 128, 2048) == att(16, 128)    # each query its own tokens: 4 rows
-    for bad in ((0, 1, 32, 8, 128, 0), (1, 0, 32, 8, 128, 0), (1, 1, 30, 8, 128, 0),
-                (1, 1, 32, 0, 128, 0), (1, 1, 32, 8, 96, 0), (1, 1, 32, 8, 128, -1),
-                (1 << 20, 1 << 12, 32, 8, 128, 0)):
+    assert f(32, 1, 32, 8, 128, 64, 512, 0) == att(16, 128)
+    assert f(32, 1, 32, 8, 64, 64, 512, 0) == att(16, 64)
+    assert f(8, 16, 32, 8, 128, 64, 512, 0) == att(32, 128)
+    assert f(8, 16, 32, 8, 128, 64, 512, 2048) == att(16, 128)   # each query its own tokens
+    assert f(1, 1, 16, 2, 128, 16, 50, 0) == 0                   # a cluster per item: no partials
+    for bad in ((0, 1, 32, 8, 128, 64, 512, 0), (1, 0, 32, 8, 128, 64, 512, 0),
+                (1, 1, 30, 8, 128, 64, 512, 0), (1, 1, 32, 0, 128, 64, 512, 0),
+                (1, 1, 32, 8, 96, 64, 512, 0), (1, 1, 32, 8, 128, 64, 512, -1),
+                (1, 1, 32, 8, 128, 0, 512, 0), (1, 1, 32, 8, 128, 64, 0, 0),
+                (1 << 20, 1 << 12, 32, 8, 128, 64, 512, 0)):
         assert f(*bad) == 0, bad
     g = c.misa_pages_workspace_size
-    assert g(4, 8, 1000) == a256(32) + 3 * a256(4000) + 3 * a256(16)
-    assert g(100, 1000, 10) == 100 * 1000 * 4 + (-100 * 1000 * 4) % 256
-    for bad in ((0, 8, 10), (4, 0, 10), (4, 8, 0), (4, 8, (1 << 30) + 1)):
-        assert g(*bad) == 0, bad
+    for op in (7, 9):                        # resize, compact
+        assert g(op, 4, 8, 1000) == a256(32) + 3 * a256(4000) + 3 * a256(16)
+    assert g(8, 100, 300, 10) == 0           # fork: a table that one cluster holds
+    assert g(8, 100, 1000, 10) == a256(100 * 1000 * 4)
+    for op in (7, 8, 9):
+        for bad in ((0, 8, 10), (4, 0, 10), (4, 8, 0), (4, 8, (1 << 30) + 1), (1 << 16, 1 << 15, 9)):
+            assert g(op, *bad) == 0, bad
+    assert g(6, 4, 8, 1000) == 0
 
 
 def _attention(c, dtype=0, nseq=2, T=1, Hq=8, Hkv=2, d=128, num_pages=16, page_size=16,
