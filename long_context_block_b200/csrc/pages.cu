@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <utility>
 
 #include "internal.h"
 #include "misa.h"
@@ -35,11 +36,12 @@ constexpr int kCopyBytes = kApplyThreads * 16 * kCopyUnroll;   // piece of a pag
 
 // Scratch of resize and compact (256-aligned regions).
 struct PlanScratch {
-  int* head;      // [8]: copies, n_live, whether the call goes ahead
+  int* head;      // [8]: page copies; compact: n_live; resize: whether the call goes ahead
   int* list;      // [num_pages]: resize: the lowest free pages; compact: the holes below n_live
   int* list2;     // [num_pages]: resize: holders of a page that grow; compact: live pages from
                   // n_live on, at their rank among the live ones
-  int* map;       // [num_pages]: resize: the last holder that grows; compact: where a page goes
+  int* map;       // [num_pages]: resize: the last holder that grows; compact: the rank of a live
+                  // page from n_live on, -1 of a free one
   int* first;     // [nseq]: rank of the first page that a sequence takes
   int* cow;       // [nseq]: page to copy, -1: none
   int* cow_seq;   // [nseq]: the sequences that copy, in order
@@ -412,6 +414,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   if (tid == 0) {
     s_live = live;
     s_holes = 0;
+    if (rank == 0) s.head[0] = 0;
   }
   cluster.sync();
   int before = 0, n_live = 0;
@@ -421,47 +424,43 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     if (r < rank) before += f;
     n_live += f;
   }
-  // hole i below n_live goes to list[i]; the live page of rank i from n_live on to list2[i]
+  auto token = cluster.barrier_arrive();   // this CTA reads no other's shared memory any more
   int holes = 0;
   rank_slice<false>(refs, lo, hi, before, INT_MAX, s_bits, s_at, s_scan,
                     [&](int p, bool is_live, int at) {
-                      if (p < n_live) {
-                        if (!is_live) {
-                          s.list[p - at] = p;
-                          ++holes;
-                        }
-                      } else {
+                      if (p >= n_live) {
                         if (is_live) s.list2[at] = p;
-                        s.map[p] = -1;
+                        s.map[p] = is_live ? at : -1;
+                      } else if (!is_live) {
+                        s.list[p - at] = p;
+                        ++holes;
                       }
                     });
-  int sum;
-  block_scan(holes, s_scan, &sum);
-  if (tid == 0) s_holes = sum;
-  cluster.sync();
-  int moves = 0;
-#pragma unroll
-  for (int r = 0; r < kPlanCtas; ++r) moves += *cluster.map_shared_rank(&s_holes, r);
-  for (int i = rank * kPlanThreads + tid; i < moves; i += kPlanCtas * kPlanThreads) {
-    const int src = __ldcg(s.list2 + n_live - moves + i), dst = __ldcg(s.list + i);
-    s.map[src] = dst;
-    out_refs[dst] = refs[src];
-    out_refs[src] = 0;
+  if (holes) atomicAdd(&s_holes, holes);
+  __syncthreads();
+  if (tid == 0) {
+    if (s_holes) atomicAdd(s.head, s_holes);
+    if (rank == 0) {
+      s.head[1] = n_live;
+      if (n_live_out) *n_live_out = n_live;
+    }
   }
-  if (rank == 0 && tid == 0) {
-    s.head[0] = moves;
-    s.head[1] = n_live;
-    if (n_live_out) *n_live_out = n_live;
-  }
-  cluster.sync();
+  cluster.barrier_wait(std::move(token));
 }
 
 __global__ void __launch_bounds__(kApplyThreads, 4)
-    compact_apply_kernel(const int32_t* table, int entries, int num_pages,
+    compact_apply_kernel(const int32_t* table, const int32_t* refs, int entries, int num_pages,
                          const __grid_constant__ PagePools pools, int pieces, int32_t* out_table,
-                         PlanScratch s, int* status) {
+                         int32_t* out_refs, PlanScratch s, int* status) {
   pdl_prologue();
   const int moves = s.head[0], n_live = s.head[1];
+  const int stay = n_live - moves;   // live pages below n_live
+  for (int m = blockIdx.x * kApplyThreads + threadIdx.x; m < moves;
+       m += gridDim.x * kApplyThreads) {
+    const int src = s.list2[stay + m];
+    out_refs[s.list[m]] = refs[src];
+    out_refs[src] = 0;
+  }
   for (int i = blockIdx.x * kApplyThreads + threadIdx.x; i < entries;
        i += gridDim.x * kApplyThreads) {
     const int was = table[i];
@@ -469,17 +468,17 @@ __global__ void __launch_bounds__(kApplyThreads, 4)
     if (was < -1 || was >= num_pages) {
       set_status(status, MISA_ERR_BAD_DEVICE_INPUT);
     } else if (was >= n_live) {
-      now = s.map[was];
-      if (now < 0) {   // the table names a page that refs says is free
+      const int at = s.map[was];
+      if (at >= 0)
+        now = s.list[at - stay];
+      else   // the table names a page that refs says is free
         set_status(status, MISA_ERR_BAD_DEVICE_INPUT);
-        now = was;
-      }
     }
     if (now != was || out_table != table) out_table[i] = now;
   }
   if (pools.n > 0)
     copy_pages(pools, pieces, moves, [&](int m, int* src, int* dst) {
-      *src = s.list2[n_live - moves + m];
+      *src = s.list2[stay + m];
       *dst = s.list[m];
     });
 }
@@ -507,13 +506,12 @@ __device__ __forceinline__ void fork_read(const ForkArgs& a, int i, int& was, in
 }
 
 // The counts follow; an entry that stays the same touches none.
-__device__ __forceinline__ void fork_write(const ForkArgs& a, int i, int was, int now) {
+__device__ __forceinline__ void fork_count(const ForkArgs& a, int was, int now) {
   if (was < -1 || was >= a.num_pages) set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
   if (now != was) {
     if ((unsigned)now < (unsigned)a.num_pages) atomicAdd(a.out_refs + now, 1);
     if ((unsigned)was < (unsigned)a.num_pages) atomicSub(a.out_refs + was, 1);
   }
-  if (now != was || a.out_table != a.table) a.out_table[i] = now;
 }
 
 // A table of at most kPlanCtas * kPlanThreads * kForkUnroll entries by one cluster: everything is
@@ -533,31 +531,61 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   cluster.sync();
 #pragma unroll
   for (int u = 0; u < kForkUnroll; ++u)
-    if (at + u * kStep < a.entries) fork_write(a, at + u * kStep, was[u], now[u]);
+    if (at + u * kStep < a.entries) {
+      fork_count(a, was[u], now[u]);
+      a.out_table[at + u * kStep] = now[u];
+    }
 }
 
+// Any table, V entries (of one row) a thread and step.  The counts bound it: an entry that changes
+// costs two atomic updates at random places, 0.75 M of each 4 us (1024 rows of 2048 entries, half
+// of the rows changing: 9 us without the counts).
+template <int V>
 __global__ void __launch_bounds__(kApplyThreads) fork_kernel(const ForkArgs a) {
   pdl_prologue();
-  const int step = gridDim.x * kApplyThreads;
-  for (int64_t i0 = blockIdx.x * kApplyThreads + threadIdx.x; i0 < a.entries;
-       i0 += (int64_t)step * kForkUnroll) {
-    int was[kForkUnroll], now[kForkUnroll];
+  const int words = a.entries / V, step = gridDim.x * kApplyThreads;
+  for (int w = blockIdx.x * kApplyThreads + threadIdx.x; w < words; w += step) {
+    const int i = w * V, n = a.by_row(i);
+    int from = a.parent[n];
+    if (from < -1 || from >= a.nseq) {
+      set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
+      from = n;
+    }
+    int was[V], now[V];
+    if constexpr (V == 4) {
+      *reinterpret_cast<int4*>(was) = *reinterpret_cast<const int4*>(a.table + i);
+      if (from == n)
+        *reinterpret_cast<int4*>(now) = *reinterpret_cast<const int4*>(was);
+      else if (from < 0)
+        *reinterpret_cast<int4*>(now) = make_int4(-1, -1, -1, -1);
+      else
+        *reinterpret_cast<int4*>(now) =
+            *reinterpret_cast<const int4*>(a.table + i + (from - n) * a.max_pages);
+      *reinterpret_cast<int4*>(a.out_table + i) = *reinterpret_cast<const int4*>(now);
+    } else {
+      was[0] = a.table[i];
+      now[0] = from < 0 ? -1 : a.table[i + (from - n) * a.max_pages];
+      a.out_table[i] = now[0];
+    }
 #pragma unroll
-    for (int u = 0; u < kForkUnroll; ++u)
-      if (i0 + (int64_t)u * step < a.entries) fork_read(a, (int)(i0 + u * step), was[u], now[u]);
-#pragma unroll
-    for (int u = 0; u < kForkUnroll; ++u)
-      if (i0 + (int64_t)u * step < a.entries) fork_write(a, (int)(i0 + u * step), was[u], now[u]);
+    for (int v = 0; v < V; ++v) fork_count(a, was[v], now[v]);
   }
 }
 
-// 32-bit words from one buffer to another, neither overlapping the other.
+// 32-bit words from one buffer to another, neither overlapping the other; V = 4: 16-byte aligned.
+template <int V>
 __global__ void __launch_bounds__(kApplyThreads)
     copy_words_kernel(const int32_t* __restrict__ from, int32_t* __restrict__ to, int n) {
   pdl_prologue();
-  for (int64_t i = blockIdx.x * kApplyThreads + threadIdx.x; i < n;
-       i += gridDim.x * kApplyThreads)
-    to[i] = from[i];
+  const int step = gridDim.x * kApplyThreads, first = blockIdx.x * kApplyThreads + threadIdx.x;
+  if constexpr (V == 4) {
+#pragma unroll 4
+    for (int i = first; i < n / 4; i += step)
+      reinterpret_cast<int4*>(to)[i] = reinterpret_cast<const int4*>(from)[i];
+    if (first < n % 4) to[n / 4 * 4 + first] = from[n / 4 * 4 + first];
+  } else {
+    for (int i = first; i < n; i += step) to[i] = from[i];
+  }
 }
 
 template <typename... KArgs, typename... Args>
@@ -596,6 +624,15 @@ int apply_grid(int64_t entries, int64_t copies, const PagePools* pools, int piec
   return (int)(n < 148 * 8 ? n : 148 * 8);
 }
 
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+cudaError_t copy_words(const int32_t* from, int32_t* to, int n, cudaStream_t st) {
+  const bool wide = n >= 4 && aligned16(from) && aligned16(to);
+  return launch_pdl(wide ? copy_words_kernel<4> : copy_words_kernel<1>,
+                    dim3(apply_grid(wide ? n / 4 : n, 0, nullptr, 0)), dim3(kApplyThreads), 0, st,
+                    from, to, n);
+}
+
 }  // namespace
 
 size_t pages_ws_bytes(int nseq, int num_pages) { return plan_scratch(nseq, num_pages, nullptr, nullptr); }
@@ -631,17 +668,16 @@ cudaError_t launch_pages_fork(const int32_t* table, const int32_t* refs, const i
   if (a.entries <= kSmallEntries && num_pages <= kSmallPages)
     return launch_plan(fork_small_kernel, st, a, refs);
   cudaError_t e = cudaSuccess;
-  if (out_refs != refs)
-    e = launch_pdl(copy_words_kernel, dim3(apply_grid(num_pages, 0, nullptr, 0)),
-                   dim3(kApplyThreads), 0, st, refs, out_refs, num_pages);
+  if (out_refs != refs) e = copy_words(refs, out_refs, num_pages, st);
   if (e == cudaSuccess && out_table == table) {   // rows read one another: in place, from a copy
-    e = launch_pdl(copy_words_kernel, dim3(apply_grid(a.entries, 0, nullptr, 0)),
-                   dim3(kApplyThreads), 0, st, table, static_cast<int32_t*>(scratch), a.entries);
+    e = copy_words(table, static_cast<int32_t*>(scratch), a.entries, st);
     a.table = static_cast<const int32_t*>(scratch);
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(fork_kernel, dim3(apply_grid(a.entries, 0, nullptr, 0)), dim3(kApplyThreads),
-                    0, st, a);
+  const bool wide = max_pages % 4 == 0 && aligned16(a.table) && aligned16(out_table);
+  return launch_pdl(wide ? fork_kernel<4> : fork_kernel<1>,
+                    dim3(apply_grid(a.entries / (wide ? 4 : 1), 0, nullptr, 0)),
+                    dim3(kApplyThreads), 0, st, a);
 }
 
 cudaError_t launch_pages_compact(const int32_t* table, const int32_t* refs, int nseq,
@@ -655,8 +691,8 @@ cudaError_t launch_pages_compact(const int32_t* table, const int32_t* refs, int 
   const int pieces = pieces_of(pools);
   const int entries = nseq * max_pages;
   return launch_pdl(compact_apply_kernel, dim3(apply_grid(entries, num_pages / 2, &pools, pieces)),
-                    dim3(kApplyThreads), 0, st, table, entries, num_pages, pools, pieces,
-                    out_table, s, status);
+                    dim3(kApplyThreads), 0, st, table, refs, entries, num_pages, pools, pieces,
+                    out_table, out_refs, s, status);
 }
 
 }  // namespace misa
