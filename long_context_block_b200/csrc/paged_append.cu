@@ -1,7 +1,10 @@
 // K10: the keys and values of new tokens copied into their pages of the cache: row (n, t) goes to
 // token pos[n, t] of sequence n.  HBM-bound: every byte is read once and written once.  A thread
 // moves U 16-byte pieces: their loads, the position and the page entry are all in flight before
-// the first store.
+// the first store.  U = 4 with streaming stores: 40.4 us for the 241 MB of four prompt chunks (5.97
+// TB/s, 91% of the measured copy rate; U = 2 44.6, U = 8 53.0, plain stores 41.9 us).  A decode
+// step's few rows take U = 1 and plain stores, as the attention after it reads them: 1.6 us for 32
+// rows of 8 heads, a launch.
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -52,7 +55,13 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
                      : cache_row(table + (int64_t)(row[u] / T) * max_pages, p[u], page_size, by_page, num_pages, status);
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (at[u] >= 0) dst[(int64_t)at[u] * per_row + c[u]] = x[u];
+    if (at[u] >= 0) {
+      uint4* to = dst + (int64_t)at[u] * per_row + c[u];
+      if (U > 1)
+        __stcs(to, x[u]);
+      else
+        *to = x[u];
+    }
 }
 
 }  // namespace

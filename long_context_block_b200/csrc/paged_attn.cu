@@ -44,7 +44,9 @@ constexpr int kMaxCluster = 8;     // the largest portable cluster
 // CTAs of larger clusters than pairs that are resident at once: a cluster stays within one group
 // of SMs, which leaves 264 to 284 of the 296 places (cudaOccupancyMaxActiveClusters, sizes 3 - 8).
 constexpr int kClusterCtas = 256;
-constexpr int kClusterUnits = 16;  // units per CTA up to which a cluster shares an item
+// Units that starting on an item costs, when ranges are cut (about 3 us; 32 ragged sequences of up
+// to 8192 tokens, where one range held ten short items: 92 against 103 us without).
+constexpr int kItemCost = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -502,16 +504,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_prologue();
 
-  // ---- this CTA's range of units
+  // ---- this CTA's range.  An item of u units costs kItemCost + u: the cost of starting on it
+  // (lookups, filling the ring, the warps' join) comes first.
   const int ne = (SEL ? a.nseq * a.T : a.nseq) * a.nb;
   const int chunk = (ne + kThreads - 1) / kThreads;
-  const int per = SEL ? (a.topk + UNIT - 1) / UNIT * a.Hkv : 0;   // units of an entry
-  auto units_of = [&](int i) {
-    return max(1, (Entry<RB, SEL>(a, i).tokens(a) + UNIT - 1) / UNIT) * a.Hkv;
+  const int cta = blockIdx.x;
+  const int per = SEL ? (kItemCost + (a.topk + UNIT - 1) / UNIT) * a.Hkv : 0;   // cost of an entry
+  auto cost_of = [&](int i) {
+    return (kItemCost + max(1, (Entry<RB, SEL>(a, i).tokens(a) + UNIT - 1) / UNIT)) * a.Hkv;
   };
   long long mine = 0, before = 0, total = (long long)ne * per;
   if (!SEL) {
-    for (int i = tid * chunk; i < min(ne, (tid + 1) * chunk); ++i) mine += units_of(i);
+    for (int i = tid * chunk; i < min(ne, (tid + 1) * chunk); ++i) mine += cost_of(i);
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -527,24 +531,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs 
       total += s_red[w];
     }
   }
-  const int nc = (int)min((long long)gridDim.x, total);   // CTAs with work: each at least a unit
-  const int cta = blockIdx.x;
+  const int nc = (int)min((long long)gridDim.x, total);   // CTAs with a share: each at least 1
   if (cta >= nc) {
     if (tid == 0) a.split[cta] = make_int2(-1, 0);
     return;
   }
-  const long long u0 = cta * total / nc, u1 = (cta + 1) * total / nc;
+  const long long x0 = cta * total / nc, x1 = (cta + 1) * total / nc;
   int e;
-  long long off;   // units of entry e before u
+  long long off;   // from the start of entry e to x
   if constexpr (SEL) {
-    e = (int)(u0 / per);
-    off = u0 - (long long)e * per;
+    e = (int)(x0 / per);
+    off = x0 - (long long)e * per;
   } else {
-    if (u0 >= before && u0 < before + mine) {
-      off = u0 - before;
+    if (x0 >= before && x0 < before + mine) {
+      off = x0 - before;
       e = tid * chunk;
-      for (int u = units_of(e); off >= u; u = units_of(e)) {
-        off -= u;
+      for (int n = cost_of(e); off >= n; n = cost_of(e)) {
+        off -= n;
         ++e;
       }
       s_entry = e;
@@ -556,34 +559,38 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs 
   }
 
   int2 split = make_int2(-1, 0);
-  for (long long u = u0; u < u1;) {
+  for (long long x = x0; x < x1;) {
     const Entry<RB, SEL> en(a, e);
     const int ntok = en.tokens(a);
-    const int units = max(1, (ntok + UNIT - 1) / UNIT);
-    const int hk = (int)(off / units), uo = (int)(off - (long long)hk * units);
-    const int take = (int)min((long long)(units - uo), u1 - u);
-    attend<E, D, MT, SEL>(a, en, hk, uo * UNIT, min(ntok, (uo + take) * UNIT), smem, s_ml);
-    const bool whole = take == units;
-    const int slot = 2 * cta + (uo == 0 ? 1 : 0);
-    for (int i = tid; i < en.rows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-      float mm, ll;
-      const float4 acc = warp_sum<D, MT>(smem, s_ml, r, c, mm, ll);
-      if (whole) {
-        finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c) = acc;
-        if (c == 0) a.part_ml[slot * RB + r] = make_float2(mm, ll);
+    const int units = max(1, (ntok + UNIT - 1) / UNIT), cost = kItemCost + units;
+    const int hk = (int)(off / cost), at = (int)(off - (long long)hk * cost);
+    const int go = (int)min((long long)(cost - at), x1 - x);
+    const int uo = max(0, at - kItemCost), take = max(0, at + go - kItemCost) - uo;
+    if (take > 0) {
+      attend<E, D, MT, SEL>(a, en, hk, uo * UNIT, min(ntok, (uo + take) * UNIT), smem, s_ml);
+      const bool whole = take == units;
+      const int slot = 2 * cta + (uo == 0 ? 1 : 0);
+      for (int i = tid; i < en.rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+        float mm, ll;
+        const float4 acc = warp_sum<D, MT>(smem, s_ml, r, c, mm, ll);
+        if (whole) {
+          finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c) = acc;
+          if (c == 0) a.part_ml[slot * RB + r] = make_float2(mm, ll);
+        }
+      }
+      __syncthreads();   // the buffers are free for the next segment
+      if (!whole && uo == 0) {
+        // the CTA that holds position y of all costs is floor(((y + 1) nc - 1) / total); y: the
+        // item's last unit
+        split = make_int2(e * a.Hkv + hk, (int)(((x - at + cost) * nc - 1) / total));
       }
     }
-    __syncthreads();   // the buffers are free for the next segment
-    if (!whole && uo == 0) {
-      // the CTA that holds the item's last unit x is floor(((x + 1) nc - 1) / total)
-      split = make_int2(e * a.Hkv + hk, (int)(((u + units) * nc - 1) / total));
-    }
-    u += take;
-    off += take;
-    if (off == (long long)units * a.Hkv) {
+    x += go;
+    off += go;
+    if (off == (long long)cost * a.Hkv) {
       ++e;
       off = 0;
     }
@@ -592,49 +599,98 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs 
 }
 
 // Joins the partials of the items that several CTAs share, in CTA order: block (c, y) the rows
-// y * R .. of the item that starts in CTA c.  A few KB per item: latency-bound.
+// kJoinRows y .. of the item that starts in CTA c.  A few KB per item: latency-bound, so a row's
+// parts are dealt out to kJoinGroups groups of threads.
+constexpr int kJoinRows = 2, kJoinGroups = 4, kJoinBatch = 8;
+
 template <typename E, int D, int MT, bool SEL>
-__global__ void __launch_bounds__(128) paged_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinRows* kJoinGroups*(D / 4))
+    paged_join_kernel(const AttnArgs a) {
   constexpr int RB = 16 * MT;
-  constexpr int R = 128 / (D / 4);
+  constexpr int LANES = D / 4;
+  __shared__ float4 s_acc[kJoinRows * kJoinGroups][LANES];
+  __shared__ float2 s_ml[kJoinRows * kJoinGroups];
   pdl_prologue();
   const int cta = blockIdx.x;
   const int2 sp = a.split[cta];
   if (sp.x < 0) return;
   const int e = sp.x / a.Hkv, hk = sp.x - e * a.Hkv;
   const Entry<RB, SEL> en(a, e);
-  const int r = blockIdx.y * R + threadIdx.x / (D / 4), c = (threadIdx.x % (D / 4)) * 4;
-  if (r >= en.rows) return;
-  // parts: slot 2 cta + 1, then slot 2 c' of the CTAs up to sp.y
-  float mm = a.part_ml[(2 * cta + 1) * RB + r].x;
-#pragma unroll 8
-  for (int p = cta + 1; p <= sp.y; ++p) mm = fmaxf(mm, a.part_ml[2 * p * RB + r].x);
-  float ll = 0.f;
+  const int team = threadIdx.x / LANES, lane = threadIdx.x - team * LANES, c = lane * 4;
+  const int r = blockIdx.y * kJoinRows + team / kJoinGroups, group = team % kJoinGroups;
+  // parts: slot 2 cta + 1, then slot 2 p of the CTAs p up to sp.y; this group's: every fourth
+  float mm = -INFINITY, ll = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int p = cta; p <= sp.y; ++p) {
-    const int slot = p == cta ? 2 * p + 1 : 2 * p;
-    const float2 ml = a.part_ml[slot * RB + r];
-    add_part(acc, ll, mm, ml.x, ml.y,
-             *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c));
+  for (int p0 = cta + group; r < en.rows && p0 <= sp.y; p0 += kJoinGroups * kJoinBatch) {
+    float2 part[kJoinBatch];
+    float4 vals[kJoinBatch];
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) {   // all reads at once
+      const int p = p0 + i * kJoinGroups, slot = p == cta ? 2 * p + 1 : 2 * p;
+      part[i] = make_float2(-INFINITY, 0.f);
+      if (p <= sp.y) {
+        part[i] = a.part_ml[slot * RB + r];
+        vals[i] = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) {
+      if (p0 + i * kJoinGroups > sp.y) break;
+      const float2 ml = part[i];
+      const float up = fmaxf(mm, ml.x);
+      const float f = mm == up ? 1.f : exp2_approx(mm - up);
+      ll *= f;
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
+      mm = up;
+      add_part(acc, ll, mm, ml.x, ml.y, vals[i]);
+    }
   }
+  s_acc[team][lane] = acc;
+  if (lane == 0) s_ml[team] = make_float2(mm, ll);
+  __syncthreads();
+  if (group || r >= en.rows) return;
+#pragma unroll
+  for (int g = 1; g < kJoinGroups; ++g) mm = fmaxf(mm, s_ml[team + g].x);
+  ll = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int g = 0; g < kJoinGroups; ++g)
+    add_part(acc, ll, mm, s_ml[team + g].x, s_ml[team + g].y, s_acc[team + g][lane]);
   finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
 }
 
 int rows_per_item(const PagedAttn& p) { return p.topk > 0 ? p.Hq / p.Hkv : p.T * (p.Hq / p.Hkv); }
 
-// CTAs that share an item: 0 for equal ranges.
+// CTAs that share an item: 0 for equal ranges.  The longest item there can be decides, as the
+// lengths are known on the device only.
+//   Time of a unit (32 KB) per CTA: 1.48 us where all 296 CTAs stream (the memory's rate), 0.9 us
+//   where few do (latency).  Shared items pay full waves of CTAs and a last, partial one; equal
+//   ranges pay the average and about 3 us for the join: 64 items of 2048 selected tokens 17.7
+//   against 20.7 us, 360 items (two waves, the second a fifth full) 84 against 72 us.
+//   In the prefix form the lengths may differ, and a long sequence among short ones keeps its
+//   cluster alone, so 16 units a CTA are the most: 8 sequences of up to 4096 tokens (16 units) 25.4
+//   against 29.4 us when equally long and 19.8 against 17.0 us when ragged, of up to 8192 (32
+//   units) 44.0 against 49.3 and 32.1 against 19.7 us.
 int cluster_size(const PagedAttn& p) {
   const int rows = rows_per_item(p), rb = rows > 16 ? 32 : 16, unit = kWarps * (2048 / p.d);
   const int64_t items =
       (int64_t)p.nseq * (p.topk > 0 ? p.T : 1) * ((rows + rb - 1) / rb) * p.Hkv;
   const int64_t span = p.topk > 0 ? p.topk : (int64_t)p.max_pages * p.page_size;
-  const int64_t units = (span + unit - 1) / unit;   // of the longest item there can be
-  if (items > kMaxCtas) return 0;
+  const int64_t units = (span + unit - 1) / unit;
   int64_t c = (2 * items > kClusterCtas ? kMaxCtas : kClusterCtas) / items;
   if (c > kMaxCluster) c = kMaxCluster;
   if (c > units) c = units;
-  return (units + c - 1) / c <= kClusterUnits ? (int)c : 0;
+  if (c < 1) c = 1;
+  const int64_t steps = (units + c - 1) / c;   // units of a CTA
+  if (p.topk == 0 && steps > 16) return 0;
+  const int64_t full = items * c / kMaxCtas, rest = items * c % kMaxCtas;
+  const double last = rest == 0 ? 0.0 : std::fmax(0.9, 1.48 * rest / kMaxCtas);
+  const double shared = (double)steps * (1.48 * full + last);
+  const double ranges = (double)items * units * 1.48 / kMaxCtas + 3.0;
+  return shared <= ranges ? (int)c : 0;
 }
 
 template <typename E, int D, int MT, bool SEL>
@@ -672,9 +728,9 @@ cudaError_t launch_variant(const PagedAttn& p, AttnArgs a, cudaStream_t st) {
   err = launch_pdl(kernel, dim3(grid), dim3(kThreads), S::SMEM, st, a);
   if (err != cudaSuccess || units == 1) return err;
   const int most = rows < S::RB ? rows : S::RB;
-  constexpr int R = 128 / (D / 4);
-  return launch_pdl(paged_join_kernel<E, D, MT, SEL>, dim3(grid, (most + R - 1) / R), dim3(128), 0,
-                    st, a);
+  return launch_pdl(paged_join_kernel<E, D, MT, SEL>,
+                    dim3(grid, (most + kJoinRows - 1) / kJoinRows),
+                    dim3(kJoinRows * kJoinGroups * (D / 4)), 0, st, a);
 }
 
 template <typename E, int D>
