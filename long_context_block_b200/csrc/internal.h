@@ -192,6 +192,10 @@ struct PagedAttn {
 size_t paged_attn_ws_bytes(const PagedAttn& p);
 cudaError_t launch_paged_attn(const PagedAttn& p, void* scratch, int* status, cudaStream_t st);
 
+// The form for many query rows per key-value head (paged_attn_tc.cu), which the two above choose.
+size_t paged_attn_tc_ws_bytes(const PagedAttn& p);
+cudaError_t launch_paged_attn_tc(const PagedAttn& p, void* scratch, int* status, cudaStream_t st);
+
 // K10 -- new keys and values into their pages (paged_append.cu).  row_bytes: Hkv * d * 2.
 cudaError_t launch_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
                                 const int32_t* page_table, int nseq, int T, int row_bytes,

@@ -29,6 +29,15 @@ struct Divide {
   }
 };
 
+template <typename E>
+struct IsBf16 {
+  static constexpr bool value = false;
+};
+template <>
+struct IsBf16<__nv_bfloat16> {
+  static constexpr bool value = true;
+};
+
 // Two fp32 values rounded to the 16-bit type, `lo` in the lower half.
 template <typename E>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);

@@ -22,11 +22,9 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
-#include <cmath>
-
 #include "internal.h"
 #include "misa.h"
-#include "paged.cuh"
+#include "paged_attn.cuh"
 
 namespace misa {
 namespace {
@@ -44,61 +42,6 @@ constexpr int kMaxCluster = 8;     // the largest portable cluster
 // CTAs of larger clusters than pairs that are resident at once: a cluster stays within one group
 // of SMs, which leaves 264 to 284 of the 296 places (cudaOccupancyMaxActiveClusters, sizes 3 - 8).
 constexpr int kClusterCtas = 256;
-// Units that starting on an item costs, when ranges are cut (about 3 us; 32 ragged sequences of up
-// to 8192 tokens, where one range held ten short items: 92 against 103 us without).
-constexpr int kItemCost = 2;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct AttnArgs {
-  const void* q;
-  const void* k;
-  const void* v;
-  const int32_t* table;
-  const int32_t* pos;
-  const int32_t* idx;
-  void* out;
-  float* lse;
-  int* status;
-  float* part_o;   // [2 * kMaxCtas][RB][D]
-  float2* part_ml; // [2 * kMaxCtas][RB]  (maximum in the log2 domain, sum)
-  int2* split;     // [kMaxCtas]: item that starts in this CTA and ends in another (-1: none),
-                   // and the CTA it ends in
-  int nseq, T, Hq, Hkv, G, num_pages, page_size, max_pages, topk;
-  int nb;          // row blocks: per sequence (prefix form) or per query (selected form)
-  float scale2;    // |scale| log2 e, or 1 with queries of zeros
-  uint32_t q_flip; // sign bits of a query's word to flip (scale < 0)
-  uint32_t q_keep; // bits of a query's word to keep (none: scale = 0)
-  Divide by_page;  // division by page_size
-};
-
-// An entry is a row block: of a sequence's T * G rows (prefix form, r = t * G + g) or of one
-// query's G rows (selected form).
-template <int RB, bool SEL>
-struct Entry {
-  int n, row0, rows;
-  __device__ __forceinline__ Entry(const AttnArgs& a, int e) {
-    const int nq = e / a.nb, b = e - nq * a.nb;
-    if (SEL) {
-      n = nq / a.T;
-      row0 = (nq - n * a.T) * a.G + b * RB;
-      rows = min(RB, a.G - b * RB);
-    } else {
-      n = nq;
-      row0 = b * RB;
-      rows = min(RB, a.T * a.G - row0);
-    }
-  }
-  // tokens the entry walks over
-  __device__ __forceinline__ int tokens(const AttnArgs& a) const {
-    if (SEL) return a.topk;
-    int last = -1;
-    for (int t = row0 / a.G; t <= (row0 + rows - 1) / a.G; ++t)
-      last = max(last, last_token(a.pos, (int64_t)n * a.T + t, a.max_pages * a.page_size,
-                                  a.status));
-    return last + 1;
-  }
-};
 
 template <int D, int MT>
 struct Shape {
@@ -113,31 +56,6 @@ struct Shape {
   static constexpr int SMEM = RING + RB * ROWB;
   static_assert(kWarps * RB * OSTR * 4 <= RING, "the join buffer lies in the ring");
 };
-
-// One output position: 4 elements of a row, from its sum of weights and weighted values.
-template <typename E, int D>
-__device__ __forceinline__ void finish(const AttnArgs& a, int n, int rr, int hk, int c,
-                                       const float4& acc, float mm, float ll) {
-  const int t = rr / a.G, g = rr - t * a.G;
-  const int64_t head = ((int64_t)n * a.T + t) * a.Hq + hk * a.G + g;
-  const float inv = ll == 0.f ? 0.f : 1.f / ll;
-  uint2 y;
-  y.x = pack2<E>(acc.x * inv, acc.y * inv);
-  y.y = pack2<E>(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<E*>(a.out) + head * D + c) = y;
-  if (a.lse && c == 0) a.lse[head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-}
-
-// Adds a part (maximum pm, sum pl, weighted values x) under the joint maximum mm.
-__device__ __forceinline__ void add_part(float4& acc, float& ll, float mm, float pm, float pl,
-                                         const float4& x) {
-  const float f = pm == mm ? 1.f : exp2_approx(pm - (mm == -INFINITY ? 0.f : mm));
-  ll += pl * f;
-  acc.x += x.x * f;
-  acc.y += x.y * f;
-  acc.z += x.z * f;
-  acc.w += x.w * f;
-}
 
 // Tokens tok0 .. tok1 - 1 of entry `en` (of the prefix, or slots of its idx row) for key-value
 // head hk, by the whole CTA.  Leaves each warp's part in shared memory: weighted values at
@@ -496,173 +414,41 @@ template <typename E, int D, int MT, bool SEL>
 __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs a) {
   using S = Shape<D, MT>;
   constexpr int RB = S::RB, UNIT = S::UNIT;
+  using R = Range<RB, SEL, UNIT, kThreads>;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ float2 s_ml[kWarps][RB];
-  __shared__ long long s_red[kWarps];
-  __shared__ int s_entry;
-  __shared__ long long s_off;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_prologue();
-
-  // ---- this CTA's range.  An item of u units costs kItemCost + u: the cost of starting on it
-  // (lookups, filling the ring, the warps' join) comes first.
-  const int ne = (SEL ? a.nseq * a.T : a.nseq) * a.nb;
-  const int chunk = (ne + kThreads - 1) / kThreads;
+  __shared__ typename R::Shared s_range;
   const int cta = blockIdx.x;
-  const int per = SEL ? (kItemCost + (a.topk + UNIT - 1) / UNIT) * a.Hkv : 0;   // cost of an entry
-  auto cost_of = [&](int i) {
-    return (kItemCost + max(1, (Entry<RB, SEL>(a, i).tokens(a) + UNIT - 1) / UNIT)) * a.Hkv;
-  };
-  long long mine = 0, before = 0, total = (long long)ne * per;
-  if (!SEL) {
-    for (int i = tid * chunk; i < min(ne, (tid + 1) * chunk); ++i) mine += cost_of(i);
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) s_red[warp] = inc;
-    __syncthreads();
-    before = inc - mine;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_red[w];
-      total += s_red[w];
-    }
-  }
-  const int nc = (int)min((long long)gridDim.x, total);   // CTAs with a share: each at least 1
-  if (cta >= nc) {
-    if (tid == 0) a.split[cta] = make_int2(-1, 0);
-    return;
-  }
-  const long long x0 = cta * total / nc, x1 = (cta + 1) * total / nc;
-  int e;
-  long long off;   // from the start of entry e to x
-  if constexpr (SEL) {
-    e = (int)(x0 / per);
-    off = x0 - (long long)e * per;
-  } else {
-    if (x0 >= before && x0 < before + mine) {
-      off = x0 - before;
-      e = tid * chunk;
-      for (int n = cost_of(e); off >= n; n = cost_of(e)) {
-        off -= n;
-        ++e;
-      }
-      s_entry = e;
-      s_off = off;
-    }
-    __syncthreads();
-    e = s_entry;
-    off = s_off;
-  }
-
+  pdl_prologue();
+  R range;
+  typename R::Segment sg;
   int2 split = make_int2(-1, 0);
-  for (long long x = x0; x < x1;) {
-    const Entry<RB, SEL> en(a, e);
-    const int ntok = en.tokens(a);
-    const int units = max(1, (ntok + UNIT - 1) / UNIT), cost = kItemCost + units;
-    const int hk = (int)(off / cost), at = (int)(off - (long long)hk * cost);
-    const int go = (int)min((long long)(cost - at), x1 - x);
-    const int uo = max(0, at - kItemCost), take = max(0, at + go - kItemCost) - uo;
-    if (take > 0) {
-      attend<E, D, MT, SEL>(a, en, hk, uo * UNIT, min(ntok, (uo + take) * UNIT), smem, s_ml);
-      const bool whole = take == units;
-      const int slot = 2 * cta + (uo == 0 ? 1 : 0);
-      for (int i = tid; i < en.rows * (D / 4); i += kThreads) {
+  if (range.cut(a, s_range))
+    while (range.next(a, sg)) {
+      const Entry<RB, SEL> en(a, sg.e);
+      attend<E, D, MT, SEL>(a, en, sg.hk, sg.uo * UNIT, min(sg.ntok, (sg.uo + sg.take) * UNIT),
+                            smem, s_ml);
+      const bool whole = sg.take == sg.units;
+      const int slot = 2 * cta + (sg.uo == 0 ? 1 : 0);
+      for (int i = threadIdx.x; i < en.rows * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
         float mm, ll;
         const float4 acc = warp_sum<D, MT>(smem, s_ml, r, c, mm, ll);
         if (whole) {
-          finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
+          finish<E, D>(a, en.n, en.row0 + r, sg.hk, c, acc, mm, ll);
         } else {
           *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c) = acc;
           if (c == 0) a.part_ml[slot * RB + r] = make_float2(mm, ll);
         }
       }
       __syncthreads();   // the buffers are free for the next segment
-      if (!whole && uo == 0) {
-        // the CTA that holds position y of all costs is floor(((y + 1) nc - 1) / total); y: the
-        // item's last unit
-        split = make_int2(e * a.Hkv + hk, (int)(((x - at + cost) * nc - 1) / total));
-      }
+      if (!whole && sg.uo == 0) split = make_int2(sg.e * a.Hkv + sg.hk, sg.last_cta);
     }
-    x += go;
-    off += go;
-    if (off == (long long)cost * a.Hkv) {
-      ++e;
-      off = 0;
-    }
-  }
-  if (tid == 0) a.split[cta] = split;
+  if (threadIdx.x == 0) a.split[cta] = split;
 }
 
-// Joins the partials of the items that several CTAs share, in CTA order: block (c, y) the rows
-// kJoinRows y .. of the item that starts in CTA c.  A few KB per item: latency-bound, so a row's
-// parts are dealt out to kJoinGroups groups of threads.
-constexpr int kJoinRows = 2, kJoinGroups = 4, kJoinBatch = 8;
-
-template <typename E, int D, int MT, bool SEL>
-__global__ void __launch_bounds__(kJoinRows* kJoinGroups*(D / 4))
-    paged_join_kernel(const AttnArgs a) {
-  constexpr int RB = 16 * MT;
-  constexpr int LANES = D / 4;
-  __shared__ float4 s_acc[kJoinRows * kJoinGroups][LANES];
-  __shared__ float2 s_ml[kJoinRows * kJoinGroups];
-  pdl_prologue();
-  const int cta = blockIdx.x;
-  const int2 sp = a.split[cta];
-  if (sp.x < 0) return;
-  const int e = sp.x / a.Hkv, hk = sp.x - e * a.Hkv;
-  const Entry<RB, SEL> en(a, e);
-  const int team = threadIdx.x / LANES, lane = threadIdx.x - team * LANES, c = lane * 4;
-  const int r = blockIdx.y * kJoinRows + team / kJoinGroups, group = team % kJoinGroups;
-  // parts: slot 2 cta + 1, then slot 2 p of the CTAs p up to sp.y; this group's: every fourth
-  float mm = -INFINITY, ll = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = cta + group; r < en.rows && p0 <= sp.y; p0 += kJoinGroups * kJoinBatch) {
-    float2 part[kJoinBatch];
-    float4 vals[kJoinBatch];
-#pragma unroll
-    for (int i = 0; i < kJoinBatch; ++i) {   // all reads at once
-      const int p = p0 + i * kJoinGroups, slot = p == cta ? 2 * p + 1 : 2 * p;
-      part[i] = make_float2(-INFINITY, 0.f);
-      if (p <= sp.y) {
-        part[i] = a.part_ml[slot * RB + r];
-        vals[i] = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kJoinBatch; ++i) {
-      if (p0 + i * kJoinGroups > sp.y) break;
-      const float2 ml = part[i];
-      const float up = fmaxf(mm, ml.x);
-      const float f = mm == up ? 1.f : exp2_approx(mm - up);
-      ll *= f;
-      acc.x *= f;
-      acc.y *= f;
-      acc.z *= f;
-      acc.w *= f;
-      mm = up;
-      add_part(acc, ll, mm, ml.x, ml.y, vals[i]);
-    }
-  }
-  s_acc[team][lane] = acc;
-  if (lane == 0) s_ml[team] = make_float2(mm, ll);
-  __syncthreads();
-  if (group || r >= en.rows) return;
-#pragma unroll
-  for (int g = 1; g < kJoinGroups; ++g) mm = fmaxf(mm, s_ml[team + g].x);
-  ll = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int g = 0; g < kJoinGroups; ++g)
-    add_part(acc, ll, mm, s_ml[team + g].x, s_ml[team + g].y, s_acc[team + g][lane]);
-  finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
-}
-
-int rows_per_item(const PagedAttn& p) { return p.topk > 0 ? p.Hq / p.Hkv : p.T * (p.Hq / p.Hkv); }
+// More rows on a token than a warp holds: the tensor-core form (paged_attn_tc.cu).
+bool use_tc(const PagedAttn& p) { return attn_rows(p) > 32; }
 
 // CTAs that share an item: 0 for equal ranges.  The longest item there can be decides, as the
 // lengths are known on the device only.
@@ -675,7 +461,7 @@ int rows_per_item(const PagedAttn& p) { return p.topk > 0 ? p.Hq / p.Hkv : p.T *
 //   against 29.4 us when equally long and 19.8 against 17.0 us when ragged, of up to 8192 (32
 //   units) 44.0 against 49.3 and 32.1 against 19.7 us.
 int cluster_size(const PagedAttn& p) {
-  const int rows = rows_per_item(p), rb = rows > 16 ? 32 : 16, unit = kWarps * (2048 / p.d);
+  const int rows = attn_rows(p), rb = rows > 16 ? 32 : 16, unit = kWarps * (2048 / p.d);
   const int64_t items =
       (int64_t)p.nseq * (p.topk > 0 ? p.T : 1) * ((rows + rb - 1) / rb) * p.Hkv;
   const int64_t span = p.topk > 0 ? p.topk : (int64_t)p.max_pages * p.page_size;
@@ -696,7 +482,7 @@ int cluster_size(const PagedAttn& p) {
 template <typename E, int D, int MT, bool SEL>
 cudaError_t launch_variant(const PagedAttn& p, AttnArgs a, cudaStream_t st) {
   using S = Shape<D, MT>;
-  const int rows = rows_per_item(p);
+  const int rows = attn_rows(p);
   a.nb = (rows + S::RB - 1) / S::RB;
   const int64_t items = (int64_t)p.nseq * (SEL ? p.T : 1) * a.nb * p.Hkv;
   const int size = cluster_size(p);
@@ -727,15 +513,12 @@ cudaError_t launch_variant(const PagedAttn& p, AttnArgs a, cudaStream_t st) {
   const int grid = (int)(items * units < kMaxCtas ? items * units : kMaxCtas);
   err = launch_pdl(kernel, dim3(grid), dim3(kThreads), S::SMEM, st, a);
   if (err != cudaSuccess || units == 1) return err;
-  const int most = rows < S::RB ? rows : S::RB;
-  return launch_pdl(paged_join_kernel<E, D, MT, SEL>,
-                    dim3(grid, (most + kJoinRows - 1) / kJoinRows),
-                    dim3(kJoinRows * kJoinGroups * (D / 4)), 0, st, a);
+  return launch_join<E, D, S::RB, SEL>(a, grid, rows < S::RB ? rows : S::RB, st);
 }
 
 template <typename E, int D>
 cudaError_t launch_type(const PagedAttn& p, const AttnArgs& a, cudaStream_t st) {
-  const bool two = rows_per_item(p) > 16;
+  const bool two = attn_rows(p) > 16;
   if (p.topk > 0)
     return two ? launch_variant<E, D, 2, true>(p, a, st) : launch_variant<E, D, 1, true>(p, a, st);
   return two ? launch_variant<E, D, 2, false>(p, a, st) : launch_variant<E, D, 1, false>(p, a, st);
@@ -744,43 +527,14 @@ cudaError_t launch_type(const PagedAttn& p, const AttnArgs& a, cudaStream_t st) 
 }  // namespace
 
 size_t paged_attn_ws_bytes(const PagedAttn& p) {
+  if (use_tc(p)) return paged_attn_tc_ws_bytes(p);
   if (cluster_size(p)) return 0;
-  const size_t rb = rows_per_item(p) > 16 ? 32 : 16;
-  return align256(2 * kMaxCtas * rb * p.d * sizeof(float)) +
-         align256(2 * kMaxCtas * rb * sizeof(float2)) + align256(kMaxCtas * sizeof(int2));
+  return attn_ws_bytes(kMaxCtas, attn_rows(p) > 16 ? 32 : 16, p.d);
 }
 
 cudaError_t launch_paged_attn(const PagedAttn& p, void* scratch, int* status, cudaStream_t st) {
-  const size_t rb = rows_per_item(p) > 16 ? 32 : 16;
-  AttnArgs a = {};
-  a.q = p.q;
-  a.k = p.k_cache;
-  a.v = p.v_cache;
-  a.table = p.page_table;
-  a.pos = p.pos;
-  a.idx = p.idx;
-  a.out = p.out;
-  a.lse = p.lse;
-  a.status = status;
-  char* w = static_cast<char*>(scratch);
-  a.part_o = reinterpret_cast<float*>(w);
-  w += align256(2 * kMaxCtas * rb * p.d * sizeof(float));
-  a.part_ml = reinterpret_cast<float2*>(w);
-  w += align256(2 * kMaxCtas * rb * sizeof(float2));
-  a.split = reinterpret_cast<int2*>(w);
-  a.nseq = p.nseq;
-  a.T = p.T;
-  a.Hq = p.Hq;
-  a.Hkv = p.Hkv;
-  a.G = p.Hq / p.Hkv;
-  a.num_pages = p.num_pages;
-  a.page_size = p.page_size;
-  a.max_pages = p.max_pages;
-  a.topk = p.topk;
-  a.scale2 = p.scale == 0.f ? 1.f : std::fabs(p.scale) * kLog2e;
-  a.q_flip = p.scale < 0.f ? 0x80008000u : 0u;
-  a.q_keep = p.scale == 0.f ? 0u : 0xffffffffu;
-  a.by_page = Divide::by(p.page_size);
+  if (use_tc(p)) return launch_paged_attn_tc(p, scratch, status, st);
+  const AttnArgs a = attn_args(p, scratch, kMaxCtas, attn_rows(p) > 16 ? 32 : 16, status);
   if (p.dtype == MISA_DTYPE_BF16)
     return p.d == 128 ? launch_type<__nv_bfloat16, 128>(p, a, st)
                       : launch_type<__nv_bfloat16, 64>(p, a, st);

@@ -156,6 +156,19 @@ CASES = {
     "sel_group20": dict(lens=[600, 90], topk=100, Hq=20, Hkv=1, ps=48),
     "sel_group40_d64": dict(lens=[600, 90], topk=130, Hq=40, Hkv=1, d=64),
     "sel_long": dict(lens=[9000, 5000], topk=2048, Hq=8, Hkv=2, ps=64),
+    # more than 32 query rows per key-value head: the tensor-core form
+    "rows33": dict(lens=[128, 129, 300, 1], Hq=33, Hkv=1),
+    "rows127_fp16": dict(lens=[1000, 31], Hq=127, Hkv=1, dtype="fp16"),
+    "rows128": dict(lens=[700, 128, 0, 127], Hq=128, Hkv=1, ps=64),
+    "rows129_two_blocks": dict(lens=[300, 257], Hq=129, Hkv=1, d=64, dtype="fp16"),
+    "rows_draft16_group8": dict(lens=[900, 16, 130, 9, 1], T=16, Hq=16, Hkv=2, ps=7),
+    "rows_many_segments": dict(lens=[(i * 61) % 400 for i in range(90)], T=9, Hq=8, Hkv=2, d=64,
+                               ps=32),
+    "rows_long_one": dict(lens=[12000], T=5, Hq=8, Hkv=1, ps=64),
+    "rows_sel": dict(lens=[1500, 400, 0, 5], topk=700, Hq=64, Hkv=1, ps=48),
+    "rows_sel_draft": dict(lens=[600, 100], T=3, topk=129, Hq=96, Hkv=2, d=64, dtype="fp16"),
+    "rows_negative_scale": dict(lens=[300], Hq=48, Hkv=1, scale=-0.15),
+    "rows_zero_scale": dict(lens=[300], Hq=48, Hkv=1, scale=0.0),
     "negative_scale": dict(lens=[300], scale=-0.2),
     "zero_scale": dict(lens=[100], scale=0.0),
 }
