@@ -33,11 +33,32 @@ struct AttnArgs {
                    // and the CTA it ends in
   int nseq, T, Hq, Hkv, G, num_pages, page_size, max_pages, topk;
   int nb;          // row blocks: per sequence (prefix form) or per query (selected form)
+  int ctas;        // of the kernel that leaves the partials
+  int whole;       // an item for every group of CTAs, none is split
+  int side;        // row blocks that neighbouring CTAs walk side by side: nb, or 1 (one by one)
   float scale2;    // |scale| log2 e, or 1 with queries of zeros
   uint32_t q_flip; // sign bits of a query's word to flip (scale < 0)
   uint32_t q_keep; // bits of a query's word to keep (none: scale = 0)
   Divide by_page;  // division by page_size
 };
+
+// Tokens that queries t0 .. t1 of sequence n see, of the longest of their prefixes.
+__device__ __forceinline__ int longest(const AttnArgs& a, int n, int t0, int t1) {
+  const int cap = a.max_pages * a.page_size;
+  const int32_t* pos = a.pos + (int64_t)n * a.T;
+  int last = -1;
+  for (int t = t0; t <= t1; t += 8) {   // eight reads at once
+    int p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = pos[min(t + i, t1)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (p[i] < -1 || p[i] >= cap) set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
+      last = max(last, min(p[i], cap - 1));
+    }
+  }
+  return last + 1;
+}
 
 // An entry is a row block: of a sequence's T * G rows (prefix form, r = t * G + g) or of one
 // query's G rows (selected form).
@@ -59,11 +80,7 @@ struct Entry {
   // tokens the entry walks over
   __device__ __forceinline__ int tokens(const AttnArgs& a) const {
     if (SEL) return a.topk;
-    int last = -1;
-    for (int t = row0 / a.G; t <= (row0 + rows - 1) / a.G; ++t)
-      last = max(last, last_token(a.pos, (int64_t)n * a.T + t, a.max_pages * a.page_size,
-                                  a.status));
-    return last + 1;
+    return longest(a, n, row0 / a.G, (row0 + rows - 1) / a.G);
   }
 };
 
@@ -81,10 +98,12 @@ __device__ __forceinline__ void finish(const AttnArgs& a, int n, int rr, int hk,
   if (a.lse && c == 0) a.lse[head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
-// Adds a part (maximum pm, sum pl, weighted values x) under the joint maximum mm.
+// Adds a part (maximum pm, sum pl, weighted values x) under the joint maximum mm.  A part that saw
+// nothing (sum 0) adds nothing: its products may be NaN where another row's tokens were.
 __device__ __forceinline__ void add_part(float4& acc, float& ll, float mm, float pm, float pl,
                                          const float4& x) {
-  const float f = pm == mm ? 1.f : exp2_approx(pm - (mm == -INFINITY ? 0.f : mm));
+  if (pl == 0.f) return;
+  const float f = pm == mm ? 1.f : exp2_approx(pm - mm);
   ll += pl * f;
   acc.x += x.x * f;
   acc.y += x.y * f;
@@ -94,11 +113,13 @@ __device__ __forceinline__ void add_part(float4& acc, float& ll, float mm, float
 
 // The share of one CTA of NT threads in all items' units.  An item of u units costs kItemCost + u:
 // the cost of starting on it (lookups, filling the ring) comes first.  Ranges of equal cost, one
-// for each of the first nc CTAs.
+// for each of the first nc groups of a.side CTAs, whose CTAs take a row block each: they read the
+// same tokens at the same time, so that the second reads come from L2 (two blocks of 256 drafted
+// rows over 32 x 32768 tokens: NEWSIDE us, 201 us when each block was an item of its own).
 template <int RB, bool SEL, int UNIT, int NT>
 struct Range {
-  long long x, x1, total, off;   // position, end, sum of all costs; from the start of entry e to x
-  int e, nc;
+  long long x, x1, total, off;   // position, end, sum of all costs; from the start of item e to x
+  int e, nc;                     // e: counts entries, or groups of a.side entries
 
   struct Shared {
     long long sum[NT / 32], off;
@@ -113,16 +134,29 @@ struct Range {
   static __device__ __forceinline__ int units_of(int ntok) {
     return max(1, (ntok + UNIT - 1) / UNIT);
   }
+  // Tokens that the entries of group e walk over.
+  static __device__ __forceinline__ int tokens_of(const AttnArgs& a, int e) {
+    if (SEL) return a.topk;
+    if (a.side == 1) return Entry<RB, SEL>(a, e).tokens(a);
+    return longest(a, e, 0, a.T - 1);   // all rows of the sequence
+  }
 
   // Every thread of the CTA; false: no share.
   __device__ __forceinline__ bool cut(const AttnArgs& a, Shared& sh) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int ne = (SEL ? a.nseq * a.T : a.nseq) * a.nb;
+    const int ne = (SEL ? a.nseq * a.T : a.nseq) * (a.nb / a.side);
+    if (a.whole) {   // gridDim.x = side * entries * Hkv
+      const int item = blockIdx.x / a.side;
+      e = item / a.Hkv;
+      total = x1 = kItemCost + units_of(tokens_of(a, e));
+      off = (item - e * a.Hkv) * x1;
+      x = 0;
+      nc = 1;
+      return true;
+    }
     const int chunk = (ne + NT - 1) / NT;
     const int per = SEL ? (kItemCost + units_of(a.topk)) * a.Hkv : 0;   // cost of an entry
-    auto cost_of = [&](int i) {
-      return (kItemCost + units_of(Entry<RB, SEL>(a, i).tokens(a))) * a.Hkv;
-    };
+    auto cost_of = [&](int i) { return (kItemCost + units_of(tokens_of(a, i))) * a.Hkv; };
     long long mine = 0, before = 0;
     total = (long long)ne * per;
     if (!SEL) {
@@ -142,8 +176,8 @@ struct Range {
         total += sh.sum[w];
       }
     }
-    nc = (int)min((long long)gridDim.x, total);
-    const int cta = blockIdx.x;
+    nc = (int)min((long long)(gridDim.x / a.side), total);
+    const int cta = blockIdx.x / a.side;
     if (cta >= nc) return false;
     x = cta * total / nc;
     x1 = (cta + 1) * total / nc;
@@ -171,8 +205,9 @@ struct Range {
   // The next piece that holds units; false: none.
   __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
     while (x < x1) {
-      s.e = e;
-      s.ntok = Entry<RB, SEL>(a, e).tokens(a);
+      const int block = blockIdx.x % a.side;
+      s.e = e * a.side + block;
+      s.ntok = tokens_of(a, e);
       s.units = units_of(s.ntok);
       const int cost = kItemCost + s.units;
       s.hk = (int)(off / cost);
@@ -180,8 +215,8 @@ struct Range {
       const int go = (int)min((long long)(cost - at), x1 - x);
       s.uo = max(0, at - kItemCost);
       s.take = max(0, at + go - kItemCost) - s.uo;
-      // position y of all costs lies in CTA floor(((y + 1) nc - 1) / total); y: the last unit
-      s.last_cta = (int)(((x - at + cost) * nc - 1) / total);
+      // position y of all costs lies in group floor(((y + 1) nc - 1) / total); y: the last unit
+      s.last_cta = (int)(((x - at + cost) * nc - 1) / total) * a.side + block;
       x += go;
       off += go;
       if (off == (long long)cost * a.Hkv) {
@@ -194,71 +229,90 @@ struct Range {
   }
 };
 
-// Joins the partials of the items that several CTAs share, in CTA order: block (c, y) the rows
-// kJoinRows y .. of the item that starts in CTA c.  A few KB per item: latency-bound, so a row's
-// parts are dealt out to kJoinGroups groups of threads.
-constexpr int kJoinRows = 2, kJoinGroups = 4, kJoinBatch = 8;
+// Joins the partials of the items that several CTAs share, in CTA order: block (x, y) rows of the
+// x-th item that starts in one CTA and ends in another.  A few KB per item, so latency-bound:
+// every team of D / 4 threads reads up to kJoinBatch parts at once, and a row with more parts
+// gets up to kJoinTeams teams.
+constexpr int kJoinTeams = 8, kJoinBatch = 4;
 
 template <typename E, int D, int RB, bool SEL>
-__global__ void __launch_bounds__(kJoinRows* kJoinGroups*(D / 4))
-    paged_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinTeams*(D / 4)) paged_join_kernel(const AttnArgs a) {
   constexpr int LANES = D / 4;
-  __shared__ float4 s_acc[kJoinRows * kJoinGroups][LANES];
-  __shared__ float2 s_ml[kJoinRows * kJoinGroups];
+  __shared__ float4 s_acc[kJoinTeams][LANES];
+  __shared__ float2 s_ml[kJoinTeams];
+  __shared__ int s_count[kJoinTeams * LANES / 32], s_cta;
   pdl_prologue();
-  const int cta = blockIdx.x;
+  const bool direct = (int)gridDim.x == a.ctas;   // a block for every CTA
+  if (threadIdx.x == 0) s_cta = direct && a.split[blockIdx.x].x >= 0 ? (int)blockIdx.x : -1;
+  if (direct) __syncthreads();
+  for (int base = 0, before = 0; !direct && base < a.ctas; base += blockDim.x) {
+    const int i = base + threadIdx.x;
+    const bool starts = i < a.ctas && a.split[i].x >= 0;
+    const uint32_t votes = __ballot_sync(0xffffffffu, starts);
+    if ((threadIdx.x & 31) == 0) s_count[threadIdx.x >> 5] = __popc(votes);
+    __syncthreads();
+    int rank = before + __popc(votes & ((1u << (threadIdx.x & 31)) - 1u));
+    for (int w = 0; w < kJoinTeams * LANES / 32; ++w) {
+      if (w < (int)(threadIdx.x >> 5)) rank += s_count[w];
+      before += s_count[w];
+    }
+    if (starts && rank == (int)blockIdx.x) s_cta = i;
+    __syncthreads();
+  }
+  const int cta = s_cta;
+  if (cta < 0) return;
   const int2 sp = a.split[cta];
-  if (sp.x < 0) return;
   const int e = sp.x / a.Hkv, hk = sp.x - e * a.Hkv;
   const Entry<RB, SEL> en(a, e);
   const int team = threadIdx.x / LANES, lane = threadIdx.x - team * LANES, c = lane * 4;
-  const int group = team % kJoinGroups;
-  for (int r0 = blockIdx.y * kJoinRows; r0 < en.rows; r0 += gridDim.y * kJoinRows) {
-  const int r = r0 + team / kJoinGroups;
-  // parts: slot 2 cta + 1, then slot 2 p of the CTAs p up to sp.y; this group's: every fourth
-  float mm = -INFINITY, ll = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = cta + group; r < en.rows && p0 <= sp.y; p0 += kJoinGroups * kJoinBatch) {
-    float2 part[kJoinBatch];
-    float4 vals[kJoinBatch];
+  const int parts = (sp.y - cta) / a.side + 1;   // a.side CTAs apart
+  const int groups = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;   // teams of a row
+  const int group = team % groups, rows = kJoinTeams / groups;
+  for (int r0 = blockIdx.y * rows; r0 < en.rows; r0 += gridDim.y * rows) {
+    const int r = r0 + team / groups;
+    float mm = -INFINITY, ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // part 0 is slot 2 cta + 1, part k slot 2 (cta + k side); a team's are `groups` apart
+    for (int k0 = group; r < en.rows && k0 < parts; k0 += groups * kJoinBatch) {
+      float2 part[kJoinBatch];
+      float4 vals[kJoinBatch];
 #pragma unroll
-    for (int i = 0; i < kJoinBatch; ++i) {   // all reads at once
-      const int p = p0 + i * kJoinGroups, slot = p == cta ? 2 * p + 1 : 2 * p;
-      part[i] = make_float2(-INFINITY, 0.f);
-      if (p <= sp.y) {
-        part[i] = a.part_ml[slot * RB + r];
-        vals[i] = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c);
+      for (int i = 0; i < kJoinBatch; ++i) {   // all reads at once
+        const int k = k0 + i * groups, slot = k == 0 ? 2 * cta + 1 : 2 * (cta + k * a.side);
+        part[i] = make_float2(-INFINITY, 0.f);
+        vals[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < parts) {
+          part[i] = a.part_ml[slot * RB + r];
+          vals[i] = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c);
+        }
       }
-    }
+      float up = mm;
 #pragma unroll
-    for (int i = 0; i < kJoinBatch; ++i) {
-      if (p0 + i * kJoinGroups > sp.y) break;
-      const float2 ml = part[i];
-      const float up = fmaxf(mm, ml.x);
-      const float f = mm == up ? 1.f : exp2_approx(mm - up);
+      for (int i = 0; i < kJoinBatch; ++i) up = fmaxf(up, part[i].x);
+      const float f = mm == up ? 1.f : exp2_approx(mm - up);   // 0 before the first part
       ll *= f;
       acc.x *= f;
       acc.y *= f;
       acc.z *= f;
       acc.w *= f;
       mm = up;
-      add_part(acc, ll, mm, ml.x, ml.y, vals[i]);
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) add_part(acc, ll, mm, part[i].x, part[i].y, vals[i]);
     }
-  }
-  s_acc[team][lane] = acc;
-  if (lane == 0) s_ml[team] = make_float2(mm, ll);
-  __syncthreads();
-  if (group == 0 && r < en.rows) {
-#pragma unroll
-  for (int g = 1; g < kJoinGroups; ++g) mm = fmaxf(mm, s_ml[team + g].x);
-  ll = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int g = 0; g < kJoinGroups; ++g)
-    add_part(acc, ll, mm, s_ml[team + g].x, s_ml[team + g].y, s_acc[team + g][lane]);
-  finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
-  }
-  __syncthreads();
+    if (groups > 1) {
+      s_acc[team][lane] = acc;
+      if (lane == 0) s_ml[team] = make_float2(mm, ll);
+      __syncthreads();
+      if (group == 0) {
+        for (int g = 1; g < groups; ++g) mm = fmaxf(mm, s_ml[team + g].x);
+        ll = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g = 0; g < groups; ++g)
+          add_part(acc, ll, mm, s_ml[team + g].x, s_ml[team + g].y, s_acc[team + g][lane]);
+      }
+      __syncthreads();
+    }
+    if (group == 0 && r < en.rows) finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
   }
 }
 
@@ -304,15 +358,20 @@ inline AttnArgs attn_args(const PagedAttn& p, void* scratch, int ctas, int rb, i
   a.q_flip = p.scale < 0.f ? 0x80008000u : 0u;
   a.q_keep = p.scale == 0.f ? 0u : 0xffffffffu;
   a.by_page = Divide::by(p.page_size);
+  a.nb = (attn_rows(p) + rb - 1) / rb;
+  a.side = 1;
+  a.whole = 0;
   return a;
 }
 
 template <typename E, int D, int RB, bool SEL>
-cudaError_t launch_join(const AttnArgs& a, int ctas, int rows, cudaStream_t st) {
-  int y = (rows + kJoinRows - 1) / kJoinRows;
-  if (y > 16) y = 16;
-  return launch_pdl(paged_join_kernel<E, D, RB, SEL>, dim3(ctas, y),
-                    dim3(kJoinRows * kJoinGroups * (D / 4)), 0, st, a);
+cudaError_t launch_join(AttnArgs a, int ctas, int64_t items, int rows, cudaStream_t st) {
+  a.ctas = ctas;
+  const int x = (int)(items < ctas ? items : ctas);   // items that can be split
+  int y = 148 * 8 / x;                                 // blocks of the others' rows: eight an SM
+  if (y > rows) y = rows;
+  return launch_pdl(paged_join_kernel<E, D, RB, SEL>, dim3(x, y > 0 ? y : 1),
+                    dim3(kJoinTeams * (D / 4)), 0, st, a);
 }
 
 }  // namespace paged

@@ -4,15 +4,16 @@
 // kernel (about 190 TFLOP/s).
 //
 // One CTA per SM, roles by warp:
-//   warps 0 - 7   two threads per query row, half of a tile's tokens each: scores from tensor
-//                 memory, running maximum and sum, weights to shared memory as the second
-//                 product's operand; the output at the end
-//   warps 8 - 11  gather the tiles (128 tokens): page entries, then keys and values with 16-byte
+//   warps 0 - 3, 4 - 7   the weights of the first and of the second 64 tokens of a tile, a thread
+//                 per query row: scores from tensor memory, running maximum and sum, weights back
+//                 to tensor memory (over the scores) as the second product's operand.  The two
+//                 groups keep a maximum, a sum and an output of their own, joined at the end, so
+//                 that nothing is exchanged in between; two score buffers keep the next tile's
+//                 scores ready
+//   warps 8, 9 and 10, 11   gather the tiles of keys and of values: page entries, then 16-byte
 //                 asynchronous copies into the 128-byte-swizzled operand layout
-//   warp 12       one thread issues the products: S = Q K^T (two buffers, so that the next tile's
-//                 scores are made while this one's weights are) and O += P V, both with fp32 sums
-//                 in tensor memory
-// The running maximum moves only when a row's scores exceed it by more than 2^8, so that O, which
+//   warp 12       one thread issues the products S = Q K^T and O += P V, fp32 sums in tensor memory
+// A group's maximum moves only when a row's scores exceed it by more than 2^8, so that O, which
 // stays in tensor memory, is rescaled a few times per item at most; any reference gives the same
 // quotient.  Ranges and partials as in paged_attn.cu.  All waits are bounded; where one runs out
 // the CTA reports MISA_ERR_DEVICE_TIMEOUT, lets its copies and products end and frees its tensor
@@ -34,31 +35,31 @@ using namespace sm100;
 constexpr int kRows = 128;       // query rows of an item
 constexpr int kTile = 128;       // tokens of a tile
 constexpr int kSoftWarps = 8, kLoadWarps = 4;
-constexpr int kCols = kTile / 2;   // tokens of a tile that a thread has the weights of
 constexpr int kThreads = 32 * (kSoftWarps + kLoadWarps + 1);
 constexpr int kTcCtas = 148;     // one per SM
+constexpr int kWholeUnits = 4;   // tiles up to which an item stays with one CTA: no join
 constexpr int kLiveDepth = 8;
 constexpr long long kWaitCycles = 4000000000LL;   // about 2 s at the top SM clock
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 2 * kTile;            // S at columns 0 and 128
+constexpr uint32_t kTmemO = 2 * kTile;            // S at columns 0 and 128, then the groups' O
 
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;                 // operand tiles are 64 columns wide
   static constexpr int kHalf = 128 * 128;                // 128 rows of 128 bytes
   static constexpr int kTileBytes = kHalves * kHalf;
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  // keys are wanted two tiles before their values are
+  static constexpr int kKStages = D == 128 ? 3 : 5, kVStages = D == 128 ? 2 : 4;
   static constexpr int kK = 0;
-  static constexpr int kV = kK + kStages * kTileBytes;
-  static constexpr int kQ = kV + kStages * kTileBytes;
-  static constexpr int kP = kQ + kTileBytes;             // 128 rows x 128 tokens
-  static constexpr int kLive = kP + 2 * kHalf;           // [kLiveDepth][4] words
+  static constexpr int kV = kK + kKStages * kTileBytes;
+  static constexpr int kQ = kV + kVStages * kTileBytes;
+  static constexpr int kLive = kQ + kTileBytes;          // [kLiveDepth][4] words
   static constexpr int kBars = kLive + kLiveDepth * 16;
-  // kfull, kfree, vfull, vfree [kStages], sfull, sfree [2], pfull, odone, qfull, drain,
-  // live [kLiveDepth], pair [4]
-  static constexpr int kNumBars = 4 * kStages + 4 + 4 + kLiveDepth + 4;
+  // kfull, kfree [kKStages], vfull, vfree [kVStages], sfull [2], pfull [2][2], qfull, odone,
+  // joined, ofree, drain, live [kLiveDepth]
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 6 + 5 + kLiveDepth;
   static constexpr int kBytes = kBars + kNumBars * 8 + 1024;   // 1 KB alignment of the base
-  static_assert(kBytes <= 227 * 1024, "shared memory");
+  static_assert(kBytes <= 224 * 1024, "shared memory");
 };
 
 // Descriptor of an operand whose 128-byte rows run along its M or N dimension (V: a row per token,
@@ -81,11 +82,6 @@ __host__ __device__ constexpr uint32_t idesc_f32(int M, int N, bool b_mn) {
   return (1u << 4) | (type << 7) | (type << 10) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-
-#define MISA_R32(r)                                                                         \
-  r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], r[10], r[11], r[12], r[13],   \
-      r[14], r[15], r[16], r[17], r[18], r[19], r[20], r[21], r[22], r[23], r[24], r[25],   \
-      r[26], r[27], r[28], r[29], r[30], r[31]
 
 // 32 fp32 columns of the warp's 32 tensor-memory lanes, a lane per thread; the wait comes apart,
 // so that several loads are in flight.
@@ -132,6 +128,46 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
+          v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31]), "r"(taddr)
+      : "memory");
+}
+// True in one lane of a converged warp, the same one each time (tcgen05.commit tracks the products
+// of the thread that issues it).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// D[tmem] (+)= A[tmem] * B[smem desc]: A's rows are the lanes, two 16-bit elements a column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 bytes (a sector) to global memory at once; 32-byte aligned.
+__device__ __forceinline__ void store32(void* to, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Weights rise above 1 up to this factor (log2) before the running maximum follows.
 constexpr float kSlack = 8.f;
 
@@ -143,35 +179,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
   __shared__ typename R::Shared s_range;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ float s_pair[2][2][kRows];
+  __shared__ float2 s_ml[2][2][kRows];   // [segment parity][group][row]
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
-  uint64_t *kfull = bars, *kfree = kfull + C::kStages, *vfull = kfree + C::kStages,
-           *vfree = vfull + C::kStages, *sfull = vfree + C::kStages, *sfree = sfull + 2,
-           *pfull = sfree + 2, *odone = pfull + 1, *qfull = odone + 1, *drain = qfull + 1,
-           *live = drain + 1, *pair = live + kLiveDepth;
+  uint64_t *kfull = bars, *kfree = kfull + C::kKStages, *vfull = kfree + C::kKStages,
+           *vfree = vfull + C::kVStages, *sfull = vfree + C::kVStages, *pfull = sfull + 2,
+           *qfull = pfull + 4, *odone = qfull + 1, *joined = odone + 1, *ofree = joined + 1,
+           *drain = ofree + 1, *live = drain + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   volatile int* abort_flag = &s_abort;
 
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&kfull[i], 32 * kLoadWarps);
+    for (int i = 0; i < C::kKStages; ++i) {
+      mbar_init(&kfull[i], 32 * kLoadWarps / 2);
       mbar_init(&kfree[i], 1);
-      mbar_init(&vfull[i], 32 * kLoadWarps);
+    }
+    for (int i = 0; i < C::kVStages; ++i) {
+      mbar_init(&vfull[i], 32 * kLoadWarps / 2);
       mbar_init(&vfree[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sfull[i], 1);
-      mbar_init(&sfree[i], 32 * kSoftWarps);
-    }
-    mbar_init(pfull, 32 * kSoftWarps);
-    mbar_init(odone, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sfull[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&pfull[i], 32 * kSoftWarps / 2);
     mbar_init(qfull, 32 * kSoftWarps);
+    mbar_init(odone, 1);
+    mbar_init(joined, 32 * kSoftWarps);
+    mbar_init(ofree, 32 * kSoftWarps);
     mbar_init(drain, 1);
-    for (int i = 0; i < kLiveDepth; ++i) mbar_init(&live[i], kLoadWarps);
-    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
+    for (int i = 0; i < kLiveDepth; ++i) mbar_init(&live[i], kLoadWarps / 2);
     fence_barrier_init();
   }
   if (warp == kSoftWarps + kLoadWarps) tmem_alloc(&s_tmem, kTmemCols);
@@ -185,53 +221,50 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
   typename R::Segment sg;
   const bool share = range.cut(a, s_range);
   int2 split = make_int2(-1, 0);
-  auto wait = [&](uint64_t* bar, int phase) {
-    return mbar_wait(bar, phase & 1, abort_flag, a.status, kWaitCycles);
-  };
-  // a whole warp's wait: lane 0 polls, all lanes agree on the outcome
+  // A whole warp's bounded wait: every lane polls, and all leave the loop together.  (With lane 0
+  // polling alone the warp stayed diverged behind a wait that had to wait, at 0.2 us for every
+  // later shuffle: 3.3 us a tile instead of 2.0 us.)  A barrier's phases are waited for one by one
+  // by every waiter, so that its parity is never ambiguous.
   auto warp_wait = [&](uint64_t* bar, int phase) {
-    int r = 1;
-    if (lane == 0) r = wait(bar, phase);
-    r = __shfl_sync(0xffffffffu, r, 0);
-    __syncwarp();
-    return r != 0;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1))) return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, mbar_try_wait_suspend(bar, phase & 1, kSuspendNs))) {
+      const bool late = clock64() - t0 > kWaitCycles;
+      if (__any_sync(0xffffffffu, late || *abort_flag)) {
+        if (late) {
+          *abort_flag = 1;
+          set_status(a.status, MISA_ERR_DEVICE_TIMEOUT);
+        }
+        return false;
+      }
+    }
+    return true;
   };
   int g = 0;        // tiles before this segment, in every role
+  int seg = 0;      // segments with tiles before this one
   bool ok = true;
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------ scores to weights, output
-    // Warps w and w + 4 have the same rows (a warp reaches the 32 tensor-memory lanes of its
-    // number modulo 4) and each half of the columns.
-    const int row = tid % kRows, half = warp / 4, quad = warp % 4;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    int swaps = 0;
-    // max or sum over the row's two threads; x of the partner, or false
-    auto swap = [&](float x, float& other) {
-      float(*buf)[kRows] = s_pair[swaps & 1];
-      buf[half][row] = x;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pair[quad]);
-      if (!warp_wait(&pair[quad], swaps++)) return false;
-      other = buf[half ^ 1][row];
-      return true;
-    };
+    const int group = warp / 4, row = tid % kRows;   // a warp reaches the 32 tensor-memory lanes
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);   // of its number modulo 4
+    const uint32_t to = lanes + kTmemO + group * D;
     while (share && ok && range.next(a, sg)) {
       const Entry<kRows, SEL> en(a, sg.e);
       const int tok0 = sg.uo * kTile, tok1 = min(sg.ntok, (sg.uo + sg.take) * kTile);
       const int n = (tok1 - tok0 + kTile - 1) / kTile;
-      const bool mine = row < en.rows, warp_live = quad * 32 < en.rows;
+      const bool mine = row < en.rows, warp_live = warp % 4 * 32 < en.rows;
       const int rr = en.row0 + row, t = mine ? rr / a.G : 0;
       float m = -INFINITY, l = 0.f;
       if (n > 0) {
-        // the row of Q; the products of the segment before have ended (their scores are here)
+        // half of the row of Q; the products of the segment before have ended
         const uint4* q = reinterpret_cast<const uint4*>(
             static_cast<const E*>(a.q) +
             (((int64_t)en.n * a.T + t) * a.Hq + sg.hk * a.G + (rr - t * a.G)) * D);
         unsigned char* dst = smem + C::kQ + row * 128;
 #pragma unroll
         for (int c0 = 0; c0 < D / 16; ++c0) {
-          const int c = half * (D / 16) + c0;
+          const int c = group * (D / 16) + c0;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (mine) {
             x = q[c];
@@ -250,138 +283,156 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
         lim = last_token(a.pos, (int64_t)en.n * a.T + t, a.max_pages * a.page_size, nullptr);
       for (int i = 0; i < n; ++i) {
         const int gi = g + i, buf = gi & 1;
+        const uint32_t ts = lanes + buf * kTile + group * 64;
+        bool behind = i > 0;   // the product of the tile before is still to be waited for
         if (!(ok = warp_wait(&sfull[buf], gi >> 1))) break;
         tc_fence_after();
-        float s[kCols];
-        if (warp_live) {
-#pragma unroll
-          for (int c = 0; c < kCols; c += 32)
-            tmem_ld32(lanes + buf * kTile + half * kCols + c, s + c);
-#pragma unroll
-          for (int c = 0; c < kCols; c += 32) tmem_ld_wait(s + c);
-        }
         if (!(ok = warp_wait(&live[gi % kLiveDepth], gi / kLiveDepth))) break;
-        const uint2 there = *reinterpret_cast<const uint2*>(smem + C::kLive +
-                                                            (gi % kLiveDepth) * 16 + half * 8);
-        tc_fence_before();
-        mbar_arrive(&sfree[buf]);
         if (warp_live) {
-          const int s0 = tok0 + i * kTile + half * kCols;
-          if ((there.x & there.y) != 0xffffffffu || (!SEL && s0 + kCols - 1 > lim)) {
+          const uint2 there = *reinterpret_cast<const uint2*>(
+              smem + C::kLive + (gi % kLiveDepth) * 16 + group * 8);
+          const int s0 = tok0 + i * kTile + group * 64;
+          float s[64];
+          tmem_ld32(ts, s);
+          tmem_ld32(ts + 32, s + 32);
+          tmem_ld_wait(s);
+          tmem_ld_wait(s + 32);
+          if ((there.x & there.y) != 0xffffffffu || (!SEL && s0 + 63 > lim)) {
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
+            for (int c = 0; c < 64; ++c)   // what the row does not see is -inf
               if (!(((c < 32 ? there.x : there.y) >> (c & 31)) & 1u) || (!SEL && s0 + c > lim))
                 s[c] = -INFINITY;
           }
-          float mx[4];
+          float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = s[c];
-#pragma unroll
-          for (int c = 4; c < kCols; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2, other;
-          if (!(ok = swap(top, other))) break;
-          top = fmaxf(top, other);
-          if (__any_sync(0xffffffffu, top > m + kSlack)) {
+          for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+          if (__any_sync(0xffffffffu, top > m + kSlack)) {   // the maximum moves, O with it
             const float up = fmaxf(m, top), f = up == m ? 1.f : exp2_approx(m - up);
             m = up;
             l *= f;
-            if (i > 0) {
+            if (behind) {
               if (!(ok = warp_wait(odone, gi - 1))) break;
+              behind = false;
               tc_fence_after();
 #pragma unroll 1
-              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+              for (int c = 0; c < D; c += 32) {
                 float o[32];
-                tmem_ld32(lanes + kTmemO + c, o);
+                tmem_ld32(to + c, o);
                 tmem_ld_wait(o);
 #pragma unroll
                 for (int x = 0; x < 32; ++x) o[x] *= f;
-                tmem_st32(lanes + kTmemO + c, o);
+                tmem_st32(to + c, o);
               }
-              tmem_st_wait();
             }
           }
           const float base = m == -INFINITY ? 0.f : -m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t p[32];
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            s[c] = exp2_approx(fmaf(s[c], a.scale2, base));
-            sum[c & 3] += s[c];
+          for (int c = 0; c < 64; c += 2) {
+            const float x = exp2_approx(fmaf(s[c], a.scale2, base));
+            const float y = exp2_approx(fmaf(s[c + 1], a.scale2, base));
+            sum[c & 2] += x;
+            sum[(c & 2) + 1] += y;
+            p[c / 2] = pack2<E>(x, y);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st32(ts, p);   // two weights to a column, over the scores
+          tmem_st_wait();
         }
-        // the weights' buffer is free once the product before has ended
-        if (i > 0 && !(ok = warp_wait(odone, gi - 1))) break;
-        if (warp_live) {
-          unsigned char* dst = smem + C::kP + half * C::kHalf + row * 128;
-#pragma unroll
-          for (int c = 0; c < kCols / 8; ++c) {
-            const float* p = s + c * 8;
-            *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) << 4)) =
-                make_uint4(pack2<E>(p[0], p[1]), pack2<E>(p[2], p[3]), pack2<E>(p[4], p[5]),
-                           pack2<E>(p[6], p[7]));
-          }
-        }
-        fence_proxy_async_smem();
+        if (behind && !(ok = warp_wait(odone, gi - 1))) break;
         tc_fence_before();
-        mbar_arrive(pfull);
+        mbar_arrive(&pfull[2 * buf + group]);
       }
       if (!ok) break;
-      if (n > 0 && !(ok = warp_wait(odone, g + n - 1))) break;
-      tc_fence_after();
       const bool whole = sg.take == sg.units;
       const int slot = 2 * cta + (sg.uo == 0 ? 1 : 0);
+      float f[2] = {0.f, 0.f};   // factors of the groups' outputs
+      if (n > 0) {
+        s_ml[seg & 1][group][row] = make_float2(m, l);
+        mbar_arrive(joined);
+        if (!(ok = warp_wait(joined, seg)) || !(ok = warp_wait(odone, g + n - 1))) break;
+        tc_fence_after();
+        const float2 x[2] = {s_ml[seg & 1][0][row], s_ml[seg & 1][1][row]};
+        m = fmaxf(x[0].x, x[1].x);
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          // a group that saw nothing of the row adds nothing, whatever its products came to
+          if (x[k].y == 0.f) continue;
+          f[k] = x[k].x == m ? 1.f : exp2_approx(x[k].x - m);
+          l += x[k].y * f[k];
+        }
+      }
       if (warp_live) {
-        float other;
-        if (!(ok = swap(l, other))) break;
-        l += other;
-        const int gq = rr - t * a.G;
-        const int64_t head = ((int64_t)en.n * a.T + t) * a.Hq + sg.hk * a.G + gq;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t head = ((int64_t)en.n * a.T + t) * a.Hq + sg.hk * a.G + (rr - t * a.G);
+        const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;   // the caller's: 16 at least
 #pragma unroll 1
-        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+        for (int c = group * (D / 2); c < (group + 1) * (D / 2); c += 32) {
           float o[32];
-          __syncwarp();
-          if (n > 0) {
-            tmem_ld32(lanes + kTmemO + c, o);
-            tmem_ld_wait(o);
-          } else {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = 0.f;
-          }
+          for (int x = 0; x < 32; ++x) o[x] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (n > 0) {
+              float y[32];
+              __syncwarp();
+              tmem_ld32(lanes + kTmemO + k * D + c, y);
+              tmem_ld_wait(y);
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (f[k] != 0.f) o[x] = fmaf(y[x], f[k] * inv, o[x]);
+            }
           if (mine && whole) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<E*>(a.out) + head * D + c);
+            uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<E*>(a.out) + head * D + c);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float* p = o + x * 8;
-              to[x] = make_uint4(pack2<E>(p[0] * inv, p[1] * inv), pack2<E>(p[2] * inv, p[3] * inv),
-                                 pack2<E>(p[4] * inv, p[5] * inv), pack2<E>(p[6] * inv, p[7] * inv));
+            for (int x = 0; x < 32; x += 16) {
+              uint32_t y[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z) y[z] = pack2<E>(o[x + 2 * z], o[x + 2 * z + 1]);
+              if (wide) {
+                store32(out + x / 2, y);
+              } else {
+                reinterpret_cast<uint4*>(out + x / 2)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                reinterpret_cast<uint4*>(out + x / 2)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+              }
             }
           } else if (mine) {
-            float4* to =
-                reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * kRows + row) * D + c);
+            float* out = a.part_o + ((int64_t)slot * kRows + row) * D + c;
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              to[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            for (int x = 0; x < 32; x += 8)
+              store32(out + x, reinterpret_cast<const uint32_t*>(o + x));
           }
         }
-        if (mine && half == 0) {
+        if (mine && group == 0) {
           if (!whole)
             a.part_ml[slot * kRows + row] = make_float2(m, l);
           else if (a.lse)
             a.lse[head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
       }
-      tc_fence_before();   // the loads of O come before the next segment's products
+      if (n > 0) {   // the next segment's products may write O
+        tc_fence_before();
+        mbar_arrive(ofree);
+        ++seg;
+      }
       if (!whole && sg.uo == 0) split = make_int2(sg.e * a.Hkv + sg.hk, sg.last_cta);
       g += n;
     }
   } else if (warp < kSoftWarps + kLoadWarps) {
     // ------------------------------------------------------------ tiles
-    const int w = warp - kSoftWarps;
+    const int w = (warp - kSoftWarps) & 1;             // which 64 tokens of a tile
+    const bool vals = warp >= kSoftWarps + 2;          // values, or keys
     constexpr int CH = D / 8, PER = 32 / CH;   // 16-byte chunks of a row, rows of a warp-wide copy
+    constexpr int STEPS = 64 / PER;
     const int c = lane % CH;
-    const uint32_t smem0 = smem_u32(smem) + (c >> 3) * C::kHalf;
+    const int stages = vals ? C::kVStages : C::kKStages;
+    uint64_t *full = vals ? vfull : kfull, *free = vals ? vfree : kfree;
+    const uint32_t ring = smem_u32(smem) + (vals ? C::kV : C::kK) + (c >> 3) * C::kHalf;
     const int cap = a.max_pages * a.page_size;
+    int st = 0, ph = 0;   // stage and its use
     while (share && ok && range.next(a, sg)) {
       const Entry<kRows, SEL> en(a, sg.e);
       const int tok0 = sg.uo * kTile, tok1 = min(sg.ntok, (sg.uo + sg.take) * kTile);
@@ -389,8 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
       const int32_t* pages = a.table + (int64_t)en.n * a.max_pages;
       const int64_t sel_row = (int64_t)en.n * a.T + en.row0 / a.G;
       const int32_t* ids = SEL ? a.idx + sel_row * a.topk : nullptr;
-      auto token = [&](int i) -> int {
-        const int s = tok0 + i * kTile + w * 32 + lane;
+      // a lane looks up two tokens of a tile, x and x + 32: the id, a tile ahead the page entry
+      auto token = [&](int i, int x) -> int {
+        const int s = tok0 + i * kTile + w * 64 + x * 32 + lane;
         if (i >= n || s >= tok1) return -1;
         return SEL ? __ldg(ids + s) : s;
       };
@@ -406,99 +458,124 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
         page = __ldg(pages + p);
         in_page = tok - p * a.page_size;
       };
-      const char* kb = static_cast<const char*>(a.k) + (int64_t)sg.hk * (D * 2) + c * 16;
-      const char* vb = static_cast<const char*>(a.v) + (int64_t)sg.hk * (D * 2) + c * 16;
-      const int64_t tstride = (int64_t)a.Hkv * (D * 2);
-      const int tok_a = token(0);
-      int tok_b = token(1), page, in_page;
+      const char* from = static_cast<const char*>(vals ? a.v : a.k) +
+                         (int64_t)sg.hk * (D * 2) + c * 16;
+      const int tstride = a.Hkv * (D * 2);   // at most 2^16 heads
+      int tok[2] = {token(0, 0), token(0, 1)}, next[2] = {token(1, 0), token(1, 1)};
+      int page[2], in_page[2];
       if (SEL) last_sel = last_token(a.pos, sel_row, cap, a.status);
-      page_of(tok_a, page, in_page);
-      for (int i = 0; i < n; ++i) {
-        const int gi = g + i, st = gi % C::kStages, ph = gi / C::kStages;
-        int src = -1;
-        if (in_page >= 0) {
-          if ((unsigned)page < (unsigned)a.num_pages)
-            src = page * a.page_size + in_page;
-          else
-            set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
-        }
-        page_of(tok_b, page, in_page);
-        tok_b = token(i + 2);
-        const uint32_t there = __ballot_sync(0xffffffffu, src >= 0);
-        auto copy = [&](const char* from, uint32_t base) {
 #pragma unroll
-          for (int j = 0; j < 32 / PER; ++j) {
-            const int in = j * PER + lane / CH;
-            const int x = __shfl_sync(0xffffffffu, src, in);
-            const int r = w * 32 + in;
-            cp_async16_or_zero(smem0 + base + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                               from + (x >= 0 ? x * tstride : 0), x >= 0);
+      for (int x = 0; x < 2; ++x) page_of(tok[x], page[x], in_page[x]);
+      for (int i = 0; i < n; ++i) {
+        const int gi = g + i;
+        int src[2];
+        uint32_t there[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          src[x] = -1;
+          if (in_page[x] >= 0) {
+            if ((unsigned)page[x] < (unsigned)a.num_pages)
+              src[x] = page[x] * a.page_size + in_page[x];
+            else
+              set_status(a.status, MISA_ERR_BAD_DEVICE_INPUT);
           }
-        };
-        if (!(ok = warp_wait(&kfree[st], ph ^ 1))) break;
-        if (lane == 0) {
-          *reinterpret_cast<uint32_t*>(smem + C::kLive + (gi % kLiveDepth) * 16 + w * 4) = there;
+          there[x] = __ballot_sync(0xffffffffu, src[x] >= 0);
+          page_of(next[x], page[x], in_page[x]);
+          next[x] = token(i + 2, x);
+        }
+        if (!(ok = warp_wait(&free[st], ph ^ 1))) break;
+        if (!vals && lane == 0) {
+          *reinterpret_cast<uint2*>(smem + C::kLive + (gi % kLiveDepth) * 16 + w * 8) =
+              make_uint2(there[0], there[1]);
           mbar_arrive(&live[gi % kLiveDepth]);
         }
-        copy(kb, C::kK + st * C::kTileBytes);
-        cp_async_mbar_arrive(&kfull[st]);
-        if (!(ok = warp_wait(&vfree[st], ph ^ 1))) break;
-        copy(vb, C::kV + st * C::kTileBytes);
-        cp_async_mbar_arrive(&vfull[st]);
+        const uint32_t dst = ring + st * C::kTileBytes;
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+          const int in = j * PER + lane / CH;   // of the warp's 64 tokens
+          const int x = __shfl_sync(0xffffffffu, src[j * PER / 32], in & 31);
+          const int r = w * 64 + in;
+          cp_async16_or_zero(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                             from + (int64_t)max(x, 0) * tstride, x >= 0);
+        }
+        cp_async_mbar_arrive(&full[st]);
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1;
+        }
       }
       g += n;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");   // this CTA's copies land before it ends
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------ products
+    // The warp stays together; one elected lane issues.
     constexpr uint32_t id_s = idesc_f32<E>(kRows, kTile, false);
     constexpr uint32_t id_o = idesc_f32<E>(kRows, D, true);
+    // operand descriptors; a step within the operands adds to the start address (16-byte units)
     const uint32_t smem0 = smem_u32(smem);
-    int seg = 0;
+    const uint64_t q0 = desc_kmajor_sw128(smem0 + C::kQ), k0 = desc_kmajor_sw128(smem0 + C::kK),
+                   v0 = desc_mnmajor_sw128(smem0 + C::kV, C::kHalf);
+    auto scores = [&](int gi) {
+      const int st = gi % C::kKStages, buf = gi & 1;
+      if (!warp_wait(&kfull[st], gi / C::kKStages)) return false;
+      tc_fence_after();
+      fence_proxy_async_smem();   // the tile was written by cp.async
+      const uint64_t k = k0 + st * (C::kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t at = ((x >> 2) * C::kHalf + (x & 3) * 32) >> 4;
+          mma_bf16(tmem + buf * kTile, q0 + at, k + at, id_s, x > 0);
+        }
+        mma_commit(&kfree[st]);
+        mma_commit(&sfull[buf]);
+      }
+      __syncwarp();
+      return true;
+    };
     while (share && ok && range.next(a, sg)) {
       const int tok0 = sg.uo * kTile, tok1 = min(sg.ntok, (sg.uo + sg.take) * kTile);
       const int n = (tok1 - tok0 + kTile - 1) / kTile;
       if (n == 0) continue;
-      if (!(ok = wait(qfull, seg++))) break;
-      auto scores = [&](int gi) {
-        const int st = gi % C::kStages, buf = gi & 1;
-        if (!wait(&kfull[st], gi / C::kStages)) return false;
-        if (gi >= 2 && !wait(&sfree[buf], (gi >> 1) - 1)) return false;
-        tc_fence_after();
-        fence_proxy_async_smem();   // the tile was written by cp.async
-        const uint32_t k = smem0 + C::kK + st * C::kTileBytes, q = smem0 + C::kQ;
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const uint32_t at = (x >> 2) * C::kHalf + (x & 3) * 32;
-          mma_bf16(tmem + buf * kTile, desc_kmajor_sw128(q + at), desc_kmajor_sw128(k + at), id_s,
-                   x > 0);
-        }
-        mma_commit(&kfree[st]);
-        mma_commit(&sfull[buf]);
-        return true;
-      };
-      if (!(ok = scores(g))) break;
+      if (!(ok = warp_wait(qfull, seg))) break;
+      if (!(ok = scores(g)) || (n > 1 && !(ok = scores(g + 1)))) break;
+      if (seg > 0 && !(ok = warp_wait(ofree, seg - 1))) break;
       for (int i = 0; i < n; ++i) {
-        const int gi = g + i, st = gi % C::kStages;
-        if (i + 1 < n && !(ok = scores(gi + 1))) break;
-        if (!(ok = wait(&vfull[st], gi / C::kStages))) break;
-        if (!(ok = wait(pfull, gi))) break;
-        tc_fence_after();
-        fence_proxy_async_smem();
-        const uint32_t v = smem0 + C::kV + st * C::kTileBytes, p = smem0 + C::kP;
+        const int gi = g + i, st = gi % C::kVStages, buf = gi & 1;
+        if (!(ok = warp_wait(&vfull[st], gi / C::kVStages))) break;
+        const uint64_t v = v0 + st * (C::kTileBytes >> 4);
+        // The groups' weights are waited for apart: of two warps on a scheduler one is ahead by
+        // its exponentials, and so one computes while the other waits.
 #pragma unroll
-        for (int x = 0; x < kTile / 16; ++x)
-          mma_bf16(tmem + kTmemO, desc_kmajor_sw128(p + (x >> 2) * C::kHalf + (x & 3) * 32),
-                   desc_mnmajor_sw128(v + x * 2048, C::kHalf), id_o, i > 0 || x > 0);
-        mma_commit(&vfree[st]);
-        mma_commit(odone);
+        for (int k = 0; k < 2; ++k) {
+          if (!(ok = warp_wait(&pfull[2 * buf + k], gi >> 1))) break;
+          tc_fence_after();
+          fence_proxy_async_smem();
+          if (elect_one()) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)   // 16 tokens each
+              mma_bf16_ts(tmem + kTmemO + k * D, tmem + buf * kTile + k * 64 + x * 8,
+                          v + (((k * 4 + x) * 2048) >> 4), id_o, i > 0 || x > 0);
+            if (k == 1) {
+              mma_commit(&vfree[st]);
+              mma_commit(odone);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (i + 2 < n && !(ok = scores(gi + 2))) break;   // over the weights just used
       }
+      if (!ok) break;
       g += n;
+      ++seg;
     }
-    mma_commit(drain);   // completes once every product issued above has
+    if (elect_one()) mma_commit(drain);   // completes once every product issued above has
+    __syncwarp();
     const long long t0 = clock64();
-    while (!mbar_try_wait_suspend(drain, 0, kSuspendNs))
-      if (clock64() - t0 > kWaitCycles) {
+    while (!__all_sync(0xffffffffu, mbar_try_wait_suspend(drain, 0, kSuspendNs)))
+      if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) {
         set_status(a.status, MISA_ERR_DEVICE_TIMEOUT);
         break;
       }
@@ -521,14 +598,17 @@ cudaError_t launch_variant(const PagedAttn& p, AttnArgs a, cudaStream_t st) {
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (err != cudaSuccess) return err;
   const int rows = attn_rows(p);
-  a.nb = (rows + kRows - 1) / kRows;
-  const int64_t items = (int64_t)p.nseq * (SEL ? p.T : 1) * a.nb * p.Hkv;
+  // side by side where that leaves few CTAs over (16 and more of 148 are the tenth)
+  if (a.nb <= kTcCtas && kTcCtas % a.nb < 16) a.side = a.nb;
+  const int64_t items = (int64_t)p.nseq * (SEL ? p.T : 1) * (a.nb / a.side) * p.Hkv;
   const int64_t span = SEL ? p.topk : (int64_t)p.max_pages * p.page_size;
   const int64_t units = (span + kTile - 1) / kTile;   // of the longest item there can be
-  const int grid = (int)(items * units < kTcCtas ? items * units : kTcCtas);
+  const int64_t most = kTcCtas / a.side;
+  a.whole = items <= most && units <= kWholeUnits;
+  const int grid = (int)(a.whole ? items : items * units < most ? items * units : most) * a.side;
   err = launch_pdl(kernel, dim3(grid), dim3(kThreads), C::kBytes, st, a);
-  if (err != cudaSuccess || units == 1) return err;
-  return launch_join<E, D, kRows, SEL>(a, grid, rows < kRows ? rows : kRows, st);
+  if (err != cudaSuccess || a.whole || units == 1) return err;
+  return launch_join<E, D, kRows, SEL>(a, grid, items * a.side, rows < kRows ? rows : kRows, st);
 }
 
 }  // namespace
