@@ -71,6 +71,22 @@ int misa_testing_score_rows_timed(const uint16_t* q, const float* w, const uint1
                                   int H, int d, int64_t L, int h, float* scores, void* ws,
                                   size_t ws_bytes, float* kernel_ms, void* stream);
 
+/*
+ * misa_paged_attention in its form for many query rows (whose warps wait for one another), with
+ * every bounded wait shortened to wait_cycles SM clock cycles (1000 .. 4e9) and, when skip_tile
+ * >= 0, the keys of that tile (128 tokens, counted over what the first CTA walks over) never
+ * loaded, so that the waits for them run out.  The call then reports MISA_ERR_DEVICE_TIMEOUT in
+ * device_status and ends; its outputs are incomplete.  With skip_tile = -1 it computes what
+ * misa_paged_attention computes.  Returns MISA_ERR_UNSUPPORTED where misa_paged_attention takes
+ * another form.
+ */
+int misa_testing_paged_attention_wait_expiry(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+    const int32_t* pos, const int32_t* idx, int dtype, int nseq, int T, int Hq, int Hkv, int d,
+    int num_pages, int page_size, int max_pages, int topk, float scale, void* out, float* lse,
+    int32_t* device_status, void* ws, size_t ws_bytes, long long wait_cycles, int skip_tile,
+    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,11 +1,13 @@
 """MISA indexer hot path for NVIDIA B200 (sm_100a).
 
 Kernels live in libmisa_b200.so (C ABI in include/misa.h); this package is a thin
-binding plus two compositions of the entry points:
+binding plus compositions of the entry points:
 
   misa_indexer  -- pool keys, route heads, routed score + top-k   (Eqs. 4, 7-10)
   misa_dagger   -- misa_indexer with k' candidates, then the all-head re-rank (Eqs. 11-12)
   hisa_indexer  -- the HISA-style token-axis block filter the pages contrast MISA with
+  misa_sparse_attention -- an indexer's selection and the attention over it, from a paged
+                   key-value cache (misa_paged_*, misa_pages_*)
 
 Reference: "MISA: Mixture of Indexer Sparse Attention for Long-Context LLM
 Inference" (picx.dev summary page, Methodology sections 1-2).
@@ -32,6 +34,7 @@ from ._binding import (  # noqa: F401
     misa_score_rows,
     misa_score_topk,
     misa_score_topk_noalloc,
+    misa_testing_paged_attention_wait_expiry,
     misa_testing_score_rows_wait_expiry,
     misa_testing_score_rows_timed,
     misa_testing_score_simt,
@@ -71,3 +74,22 @@ def hisa_indexer(q, w, k, pos, B: int, m: int, topk: int, k_pool=None):
     if k_pool is None:
         k_pool = misa_pool_keys(k, B)
     return hisa_block_filter_topk(q, w, k, k_pool, pos, B, m, topk, return_blocks=True)
+
+
+def misa_sparse_attention(qi, w, ki, pos, B: int, h: int, topk: int, q, k_cache, v_cache,
+                          page_table, k_new=None, v_new=None, k_pool=None,
+                          kprime: int | None = None, scale: float | None = None):
+    """One step of sparse attention: the step's keys and values (k_new / v_new, when given) into
+    their pages, misa_indexer's tokens of every query (misa_dagger's with kprime), and attention
+    over them.  qi, w, ki: the indexer's queries, head weights and keys (the step's included); q:
+    the attention's queries; pos: the positions of both.  Returns (out, idx, heads)."""
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new come together")
+    if k_new is not None:
+        misa_paged_append(k_new, v_new, pos, page_table, k_cache, v_cache)
+    if kprime is None:
+        idx, _, heads = misa_indexer(qi, w, ki, pos, B, h, topk, return_vals=False, k_pool=k_pool)
+    else:
+        idx, _, _, heads = misa_dagger(qi, w, ki, pos, B, h, topk, kprime, k_pool=k_pool)
+    out = misa_paged_attention(q, k_cache, v_cache, page_table, pos, idx=idx, scale=scale)
+    return out, idx, heads

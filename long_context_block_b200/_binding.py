@@ -55,6 +55,9 @@ _SIGS = {
     "misa_paged_attention_workspace_size": (_c_sz, [_c_int] * 8),
     "misa_paged_attention": (_c_int, [_p] * 6 + [_c_int] * 10 + [ctypes.c_float] + [_p] * 4
                              + [_c_sz, _p]),
+    "misa_testing_paged_attention_wait_expiry": (
+        _c_int, [_p] * 6 + [_c_int] * 10 + [ctypes.c_float] + [_p] * 4
+        + [_c_sz, ctypes.c_longlong, _c_int, _p]),
     "misa_paged_append": (_c_int, [_p] * 4 + [_c_int] * 8 + [_p] * 4),
     "misa_pages_workspace_size": (_c_sz, [_c_int] * 4),
     "misa_pages_resize": (_c_int, [_p] * 4 + [_c_int] * 4 + [_p, _p, _c_int] + [_p] * 4
@@ -697,3 +700,24 @@ def misa_testing_score_rows_timed(q, w, k, heads, pos, scores: torch.Tensor | No
                                               nseq, T, H, d, L, h, _ptr(scores), _ptr(ws),
                                               ws.numel(), ctypes.byref(ms), _stream()))
     return float(ms.value)
+
+
+def misa_testing_paged_attention_wait_expiry(q, k_cache, v_cache, page_table, pos,
+                                             wait_cycles: int, skip_tile: int):
+    """misa_paged_attention over prefixes, in its form for many query rows, with every wait
+    bounded by wait_cycles and the keys of the first CTA's tile skip_tile never loaded (-1:
+    none).  Read the outcome with misa_check_device_status."""
+    code, (num_pages, page_size, Hkv, d) = _cache(k_cache, v_cache, page_table, pos)
+    _dev(q, "q", k_cache.dtype)
+    nseq, T, Hq, _ = q.shape
+    out = torch.zeros_like(q)
+    max_pages = page_table.shape[1]
+    nb = _attention_ws(nseq, T, Hq, Hkv, d, page_size, max_pages, 0)
+    ws = torch.zeros(max(nb, 4) // 4, dtype=torch.int32, device=q.device)
+    _check("misa_testing_paged_attention_wait_expiry",
+           _lib.misa_testing_paged_attention_wait_expiry(
+               q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+               pos.data_ptr(), None, code, nseq, T, Hq, Hkv, d, num_pages, page_size, max_pages,
+               0, d ** -0.5, out.data_ptr(), None, _STATUS.get(q.device).data_ptr(), _ptr(ws), nb,
+               int(wait_cycles), int(skip_tile), _stream()))
+    return out

@@ -7,6 +7,7 @@
 
 #include "internal.h"
 #include "misa.h"
+#include "misa_testing.h"
 
 using namespace misa;
 
@@ -110,12 +111,12 @@ size_t misa_paged_attention_workspace_size(int nseq, int T, int Hq, int Hkv, int
   return paged_attn_ws_bytes(p);
 }
 
-int misa_paged_attention(const void* q, const void* k_cache, const void* v_cache,
-                         const int32_t* page_table, const int32_t* pos, const int32_t* idx,
-                         int dtype, int nseq, int T, int Hq, int Hkv, int d, int num_pages,
-                         int page_size, int max_pages, int topk, float scale, void* out,
-                         float* lse, int32_t* device_status, void* ws, size_t ws_bytes,
-                         void* stream) {
+static int paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* page_table, const int32_t* pos, const int32_t* idx,
+                           int dtype, int nseq, int T, int Hq, int Hkv, int d, int num_pages,
+                           int page_size, int max_pages, int topk, float scale, void* out,
+                           float* lse, int32_t* device_status, void* ws, size_t ws_bytes,
+                           void* stream, const WaitProbe* probe) {
   MISA_TRY(check_cache(dtype, nseq, T, Hkv, d, num_pages, page_size, max_pages));
   MISA_TRY(check_heads(nseq, T, Hq, Hkv, topk));
   if ((idx != nullptr) != (topk > 0) || !std::isfinite(scale)) return MISA_ERR_INVALID_ARG;
@@ -130,10 +131,39 @@ int misa_paged_attention(const void* q, const void* k_cache, const void* v_cache
   MISA_TRY(check_dev(out, rows * Hq * d * 2, 16));
   MISA_TRY(check_opt(lse, rows * Hq * 4, 4));
   MISA_TRY(check_opt(device_status, 4, 4));
-  PagedAttn p = {q,   k_cache, v_cache, page_table, pos,       idx,       out,  lse,  dtype, nseq,
-                 T,   Hq,      Hkv,     d,          num_pages, page_size, max_pages,  topk,  scale};
+  PagedAttn p = {q,    k_cache, v_cache, page_table, pos, idx,       out,       lse,       dtype,
+                 nseq, T,       Hq,      Hkv,        d,   num_pages, page_size, max_pages, topk,
+                 scale, probe};
+  if (probe && !paged_attn_tc(p)) return MISA_ERR_UNSUPPORTED;
   MISA_TRY(check_scratch(ws, ws_bytes, paged_attn_ws_bytes(p)));
   return cuda_status(launch_paged_attn(p, ws, device_status, (cudaStream_t)stream));
+}
+
+int misa_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* page_table, const int32_t* pos, const int32_t* idx,
+                         int dtype, int nseq, int T, int Hq, int Hkv, int d, int num_pages,
+                         int page_size, int max_pages, int topk, float scale, void* out,
+                         float* lse, int32_t* device_status, void* ws, size_t ws_bytes,
+                         void* stream) {
+  return paged_attention(q, k_cache, v_cache, page_table, pos, idx, dtype, nseq, T, Hq, Hkv, d,
+                         num_pages, page_size, max_pages, topk, scale, out, lse, device_status,
+                         ws, ws_bytes, stream, nullptr);
+}
+
+int misa_testing_paged_attention_wait_expiry(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+    const int32_t* pos, const int32_t* idx, int dtype, int nseq, int T, int Hq, int Hkv, int d,
+    int num_pages, int page_size, int max_pages, int topk, float scale, void* out, float* lse,
+    int32_t* device_status, void* ws, size_t ws_bytes, long long wait_cycles, int skip_tile,
+    void* stream) {
+  if (wait_cycles < 1000 || wait_cycles > 4000000000LL || skip_tile < -1)
+    return MISA_ERR_INVALID_ARG;
+  WaitProbe probe;
+  probe.wait_cycles = wait_cycles;
+  probe.skip_tile = skip_tile;
+  return paged_attention(q, k_cache, v_cache, page_table, pos, idx, dtype, nseq, T, Hq, Hkv, d,
+                         num_pages, page_size, max_pages, topk, scale, out, lse, device_status,
+                         ws, ws_bytes, stream, &probe);
 }
 
 int misa_paged_append(const void* k_new, const void* v_new, const int32_t* pos,

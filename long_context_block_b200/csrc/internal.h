@@ -188,7 +188,10 @@ struct PagedAttn {
   float* lse;
   int dtype, nseq, T, Hq, Hkv, d, num_pages, page_size, max_pages, topk;
   float scale;
+  const WaitProbe* test_probe;   // tests only, nullable: the tensor-core form with this bound of
+                                 // every wait and, in CTA 0, a key tile that is never loaded
 };
+bool paged_attn_tc(const PagedAttn& p);   // whether the tensor-core form runs
 size_t paged_attn_ws_bytes(const PagedAttn& p);
 cudaError_t launch_paged_attn(const PagedAttn& p, void* scratch, int* status, cudaStream_t st);
 

@@ -541,6 +541,8 @@ cudaError_t launch_type(const PagedAttn& p, const AttnArgs& a, cudaStream_t st) 
 
 }  // namespace
 
+bool paged_attn_tc(const PagedAttn& p) { return use_tc(p); }
+
 size_t paged_attn_ws_bytes(const PagedAttn& p) {
   if (use_tc(p)) return paged_attn_tc_ws_bytes(p);
   if (cluster_size(p)) return 0;

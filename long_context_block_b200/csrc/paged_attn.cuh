@@ -37,6 +37,8 @@ struct AttnArgs {
   int whole;       // an item for every group of CTAs, none is split
   int side;        // row blocks that neighbouring CTAs walk side by side: nb, or 1 (one by one)
   float scale2;    // |scale| log2 e, or 1 with queries of zeros
+  long long wait_cycles;   // bound of every wait (tensor-core form)
+  int skip_tile;           // tests only: a tile of CTA 0 whose keys never come, -1: none
   uint32_t q_flip; // sign bits of a query's word to flip (scale < 0)
   uint32_t q_keep; // bits of a query's word to keep (none: scale = 0)
   Divide by_page;  // division by page_size
@@ -361,6 +363,8 @@ inline AttnArgs attn_args(const PagedAttn& p, void* scratch, int ctas, int rb, i
   a.nb = (attn_rows(p) + rb - 1) / rb;
   a.side = 1;
   a.whole = 0;
+  a.wait_cycles = p.test_probe ? p.test_probe->wait_cycles : 4000000000LL;   // about 2 s
+  a.skip_tile = p.test_probe ? p.test_probe->skip_tile : -1;
   return a;
 }
 

@@ -39,7 +39,6 @@ constexpr int kThreads = 32 * (kSoftWarps + kLoadWarps + 1);
 constexpr int kTcCtas = 148;     // one per SM
 constexpr int kWholeUnits = 4;   // tiles up to which an item stays with one CTA: no join
 constexpr int kLiveDepth = 8;
-constexpr long long kWaitCycles = 4000000000LL;   // about 2 s at the top SM clock
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 2 * kTile;            // S at columns 0 and 128, then the groups' O
 
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1))) return true;
     const long long t0 = clock64();
     while (!__all_sync(0xffffffffu, mbar_try_wait_suspend(bar, phase & 1, kSuspendNs))) {
-      const bool late = clock64() - t0 > kWaitCycles;
+      const bool late = clock64() - t0 > a.wait_cycles;
       if (__any_sync(0xffffffffu, late || *abort_flag)) {
         if (late) {
           *abort_flag = 1;
@@ -490,15 +489,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
           mbar_arrive(&live[gi % kLiveDepth]);
         }
         const uint32_t dst = ring + st * C::kTileBytes;
+        if (vals || gi != a.skip_tile || cta != 0) {   // always, but in a test
 #pragma unroll
-        for (int j = 0; j < STEPS; ++j) {
-          const int in = j * PER + lane / CH;   // of the warp's 64 tokens
-          const int x = __shfl_sync(0xffffffffu, src[j * PER / 32], in & 31);
-          const int r = w * 64 + in;
-          cp_async16_or_zero(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                             from + (int64_t)max(x, 0) * tstride, x >= 0);
+          for (int j = 0; j < STEPS; ++j) {
+            const int in = j * PER + lane / CH;   // of the warp's 64 tokens
+            const int x = __shfl_sync(0xffffffffu, src[j * PER / 32], in & 31);
+            const int r = w * 64 + in;
+            cp_async16_or_zero(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                               from + (int64_t)max(x, 0) * tstride, x >= 0);
+          }
+          cp_async_mbar_arrive(&full[st]);
         }
-        cp_async_mbar_arrive(&full[st]);
         if (++st == stages) {
           st = 0;
           ph ^= 1;
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
     __syncwarp();
     const long long t0 = clock64();
     while (!__all_sync(0xffffffffu, mbar_try_wait_suspend(drain, 0, kSuspendNs)))
-      if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) {
+      if (__any_sync(0xffffffffu, clock64() - t0 > a.wait_cycles)) {
         set_status(a.status, MISA_ERR_DEVICE_TIMEOUT);
         break;
       }

@@ -148,7 +148,11 @@ CASES = {
     "draft7_d64": dict(lens=[300, 5], T=7, Hq=9, Hkv=3, d=64, dtype="fp16"),
     "chunk100": dict(lens=[150, 100], T=100, Hq=4, Hkv=2, d=64),
     "many_sequences": dict(lens=[(i * 37) % 200 for i in range(200)], Hq=2, Hkv=1, d=64),
-    "long_one": dict(lens=[20000], Hq=4, Hkv=1, ps=64),
+    "ranges_long_one": dict(lens=[20000], Hq=4, Hkv=1, ps=64),
+    "ranges_ragged": dict(lens=[(i * 977) % 2100 for i in range(37)] + [9000], Hq=4, Hkv=2),
+    "ranges_group20_fp16": dict(lens=[3000, 1, 12000], Hq=20, Hkv=1, dtype="fp16", ps=48),
+    "ranges_draft4_d64": dict(lens=[3000, 2, 30000], T=4, Hq=8, Hkv=2, d=64, ps=128),
+    "ranges_sel": dict(lens=[1600] * 90, topk=1500, Hq=8, Hkv=4, d=64),
     "sel": dict(lens=[1000, 300, 40], topk=64),
     "sel_one": dict(lens=[50, 1], topk=1),
     "sel_more_than_tokens": dict(lens=[40, 0, 3], topk=128),
@@ -156,27 +160,62 @@ CASES = {
     "sel_group20": dict(lens=[600, 90], topk=100, Hq=20, Hkv=1, ps=48),
     "sel_group40_d64": dict(lens=[600, 90], topk=130, Hq=40, Hkv=1, d=64),
     "sel_long": dict(lens=[9000, 5000], topk=2048, Hq=8, Hkv=2, ps=64),
-    # more than 32 query rows per key-value head: the tensor-core form
+    # more than 32 query rows per key-value head, little work: clusters over several row blocks
     "rows33": dict(lens=[128, 129, 300, 1], Hq=33, Hkv=1),
     "rows127_fp16": dict(lens=[1000, 31], Hq=127, Hkv=1, dtype="fp16"),
-    "rows128": dict(lens=[700, 128, 0, 127], Hq=128, Hkv=1, ps=64),
-    "rows129_two_blocks": dict(lens=[300, 257], Hq=129, Hkv=1, d=64, dtype="fp16"),
     "rows_draft16_group8": dict(lens=[900, 16, 130, 9, 1], T=16, Hq=16, Hkv=2, ps=7),
-    "rows_many_segments": dict(lens=[(i * 61) % 400 for i in range(90)], T=9, Hq=8, Hkv=2, d=64,
-                               ps=32),
-    "rows_long_one": dict(lens=[12000], T=5, Hq=8, Hkv=1, ps=64),
     "rows_sel": dict(lens=[1500, 400, 0, 5], topk=700, Hq=64, Hkv=1, ps=48),
-    "rows_sel_draft": dict(lens=[600, 100], T=3, topk=129, Hq=96, Hkv=2, d=64, dtype="fp16"),
     "rows_negative_scale": dict(lens=[300], Hq=48, Hkv=1, scale=-0.15),
-    "rows_zero_scale": dict(lens=[300], Hq=48, Hkv=1, scale=0.0),
+    # the same, the tensor-core form: one tile; an item per CTA; ranges that span items
+    "tc_one_tile": dict(lens=[90, 1, 0, 33, 77], Hq=40, Hkv=1, ps=8),
+    "tc_one_tile_d64_fp16": dict(lens=[90, 1, 0, 33, 77], T=9, Hq=8, Hkv=2, d=64, ps=8,
+                                 dtype="fp16"),
+    "tc_one_tile_sel": dict(lens=[3000, 100, 0], topk=128, Hq=80, Hkv=1, ps=48),
+    "tc_whole_items": dict(lens=[400 - 9 * i for i in range(40)], Hq=100, Hkv=1, ps=7),
+    "tc_whole_items_draft": dict(lens=[7 * i for i in range(60)], T=16, Hq=8, Hkv=1, d=64, ps=32,
+                                 dtype="fp16"),
+    "tc_whole_sel": dict(lens=[900 - 20 * i for i in range(40)], topk=300, Hq=128, Hkv=1, ps=64),
+    "tc_ranges": dict(lens=[900 - 9 * i for i in range(60)], Hq=128, Hkv=1, ps=64),
+    "tc_ranges_fp16_draft": dict(lens=[(i * 61) % 700 for i in range(90)], T=16, Hq=8, Hkv=2,
+                                 ps=100, dtype="fp16"),
+    "tc_ranges_d64": dict(lens=[1500 - 13 * i for i in range(70)], Hq=128, Hkv=1, d=64, ps=16),
+    "tc_long_one": dict(lens=[70000], T=5, Hq=8, Hkv=1, ps=64),
+    "tc_two_blocks_side_by_side": dict(lens=[2300 - 40 * i for i in range(20)], T=16, Hq=12,
+                                       Hkv=1, d=64, ps=32),
+    "tc_many_blocks": dict(lens=[700, 650, 0, 90], T=600, Hq=4, Hkv=1, d=64, ps=64),
+    "tc_sel_ranges": dict(lens=[3000, 2000, 900, 2500, 1000, 2800], T=6, topk=900, Hq=128,
+                          Hkv=1, ps=64),
+    "tc_sel_ranges_d64_two_blocks": dict(lens=[2500] * 20, T=3, topk=1000, Hq=160, Hkv=1, d=64,
+                                         dtype="fp16"),
+    "tc_negative_scale": dict(lens=[100], spare_slots=0, Hq=48, Hkv=1, scale=-0.15),
+    "tc_zero_scale": dict(lens=[100], spare_slots=0, Hq=48, Hkv=1, scale=0.0),
     "negative_scale": dict(lens=[300], scale=-0.2),
     "zero_scale": dict(lens=[100], scale=0.0),
 }
 
 
+def form(M, c):
+    """Which kernel a case takes, by the workspace that it asks for."""
+    from long_context_block_b200 import _binding as b
+    n, T, Hq, d = c.q.shape
+    a256 = lambda x: (x + 255) // 256 * 256
+    size = lambda ctas, rb: (a256(2 * ctas * rb * d * 4) + a256(2 * ctas * rb * 8)
+                             + a256(ctas * 8))
+    nb = b.library().misa_paged_attention_workspace_size(
+        n, T, Hq, c.k.shape[2], d, c.ps, c.table.shape[1], c.topk)
+    return {0: "cluster", size(148, 128): "tc", size(296, 16): "ranges",
+            size(296, 32): "ranges"}[nb]
+
+
 @pytest.mark.parametrize("name", list(CASES))
 def test_attention(M, name):
     c = Case(**CASES[name])
+    if name.startswith("tc_"):
+        assert form(M, c) == "tc"
+    elif name.startswith("ranges_"):
+        assert form(M, c) == "ranges"
+    elif name.startswith("rows"):
+        assert form(M, c) == "cluster"
     out, lse = c.run(M)
     torch.cuda.synchronize()
     assert M.misa_check_device_status(out.device) == 0
@@ -647,3 +686,163 @@ def test_upkeep_in_a_graph(M):
         assert mid_t.cpu().tolist() == want[0] and mid_r.cpu().tolist() == want[1]
         assert t.cpu().tolist() == table and r.cpu().tolist() == refs
     assert M.misa_check_device_status("cuda") == 0
+
+
+# ------------------------------------------------------------------------------------- together
+
+def test_sparse_decode_with_beams_and_drafts(M):
+    """The operators as a decoder uses them: prompts into fresh pages, beams forked from them,
+    drafts of three tokens with copy on write, selection by the indexer, attention over the
+    selection, rejected tokens given back, beams reordered, the pool compacted.  The reference
+    keeps every row's keys and values in plain arrays."""
+    rng = np.random.default_rng(11)
+    ps, Hkv, Hq, d, H, T, R = 16, 2, 8, 128, 8, 3, 4
+    num, mp, Lmax, topk, B, h = 80, 12, 192, 24, 16, 3
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).bfloat16()
+    k_cache = torch.full((num, ps, Hkv, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v_cache = k_cache.clone()
+    table = torch.full((R, mp), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(num, dtype=torch.int32, device="cuda")
+    ki = bf(R, Lmax, 128).cuda() * 0.1
+    rows = [[] for _ in range(R)]                     # (key, value) of every token, fp64
+    lens = [0] * R
+
+    def resize(new):
+        M.misa_pages_resize(table, refs, i32(lens), i32(new), ps, [k_cache, v_cache],
+                            out_table=table, out_refs=refs)
+        lens[:] = new
+
+    def append(kn, vn, pos):
+        M.misa_paged_append(kn.cuda(), vn.cuda(), i32(pos), table, k_cache, v_cache)
+        for n in range(R):
+            for t in range(pos.shape[1]):
+                if pos[n, t] >= 0:
+                    assert len(rows[n]) == pos[n, t]
+                    rows[n].append((f64(kn[n, t]), f64(vn[n, t])))
+
+    def fork(parent):
+        nonlocal ki
+        M.misa_pages_fork(table, refs, i32(parent), out_table=table, out_refs=refs)
+        rows[:] = [list(rows[p]) if p >= 0 else [] for p in parent]
+        lens[:] = [lens[p] if p >= 0 else 0 for p in parent]
+        ki = ki[torch.tensor([max(p, 0) for p in parent]).cuda()].contiguous()
+
+    def step():
+        start = list(lens)
+        resize([x + T for x in lens])
+        pos = np.array([[x + t for t in range(T)] for x in start], dtype=np.int32)
+        kn, vn, q = bf(R, T, Hkv, d), bf(R, T, Hkv, d), 2 * bf(R, T, Hq, d)
+        qi, w = bf(R, T, H, 128) * 0.1, torch.from_numpy(rng.standard_normal((R, T, H))).float()
+        for n in range(R):
+            ki[n, start[n]:start[n] + T] = bf(T, 128).cuda() * 0.1
+        out, idx, heads = M.misa_sparse_attention(
+            qi.cuda(), w.cuda(), ki, i32(pos), B, h, topk, q.cuda(), k_cache, v_cache, table,
+            k_new=kn.cuda(), v_new=vn.cuda())
+        for n in range(R):
+            rows[n] += [(f64(kn[n, t]), f64(vn[n, t])) for t in range(T)]
+        full, lse = M.misa_paged_attention(q.cuda(), k_cache, v_cache, table, i32(pos),
+                                           return_lse=True)
+        assert M.misa_check_device_status("cuda") == 0
+        want, _ = M.misa_score_topk(qi.cuda(), w.cuda(), ki, heads, i32(pos), topk)
+        assert torch.equal(idx, want)
+        u, e = torch.finfo(torch.bfloat16).eps / 2, 2.0 ** -23
+        for n in range(R):
+            K = np.stack([x[0] for x in rows[n]])[:, None]
+            V = np.stack([x[1] for x in rows[n]])[:, None]
+            for t in range(T):
+                for got, seen in ((out, [s for s in idx[n, t].tolist() if s >= 0]),
+                                  (full, list(range(pos[n, t] + 1)))):
+                    assert len(seen) == min(pos[n, t] + 1, topk if got is out else 10 ** 6)
+                    ref, _, mean, mag = po.attention_row(f64(q[n, t]), K, V, range(len(rows[n])),
+                                                         1, seen, d ** -0.5)
+                    w_ = u + 2 * (d + 8) * e * mag + 2.0 ** -22 + 2 * (len(seen) + 16) * e
+                    err = np.abs(f64(got[n, t]) - ref)
+                    assert np.all(err <= 1.02 * u * np.abs(ref) + w_[:, None] * mean)
+
+    # prompts of 53 and 40 tokens into rows 0 and 2, padded to one batch
+    first = [53, 0, 40, 0]
+    resize(first)
+    pos = np.full((R, 53), -1, dtype=np.int32)
+    for n, x in enumerate(first):
+        pos[n, :x] = np.arange(x)
+    append(bf(R, 53, Hkv, d), bf(R, 53, Hkv, d), pos)
+    fork([0, 0, 2, 2])
+    assert int((refs > 0).sum()) == 4 + 3 and int(refs.max()) == 2
+    step()
+    resize([x - 2 for x in lens])                     # one drafted token accepted
+    for n in range(R):
+        del rows[n][-2:]
+    fork([1, 0, 3, 3])                                # beams change places, one is dropped
+    step()
+    t, r, live = M.misa_pages_compact(table, refs, [k_cache, v_cache], out_table=table,
+                                      out_refs=refs)
+    n_live = live.item()
+    assert bool((refs[:n_live] > 0).all()) and int(refs[n_live:].abs().sum()) == 0
+    held = torch.bincount(table[table >= 0].long(), minlength=num)
+    assert torch.equal(held.int(), refs)              # every count is the holders' number
+    k_cache[n_live:] = float("nan")
+    v_cache[n_live:] = float("nan")
+    step()
+    fork([0, -1, -1, 2])
+    resize([lens[0], 0, 0, 0])
+    assert int((refs > 0).sum()) == -(-lens[0] // ps)
+
+
+def test_sparse_attention_with_the_dagger_rerank(M):
+    rng = np.random.default_rng(3)
+    f = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).bfloat16().cuda()
+    qi, ki = f(2, 1, 8, 128), f(2, 500, 128)
+    w = torch.from_numpy(rng.standard_normal((2, 1, 8))).float().cuda()
+    pos = i32([[499], [300]])
+    table = i32(rng.permutation(16).reshape(2, 8))
+    k, v, q = f(16, 64, 1, 64), f(16, 64, 1, 64), f(2, 1, 4, 64)
+    out, idx, heads = M.misa_sparse_attention(qi, w, ki, pos, 64, 2, 32, q, k, v, table, kprime=64)
+    want, _, _, h2 = M.misa_dagger(qi, w, ki, pos, 64, 2, 32, 64)
+    assert torch.equal(idx, want) and torch.equal(heads, h2)
+    assert torch.equal(out, M.misa_paged_attention(q, k, v, table, pos, idx=idx))
+    with pytest.raises(ValueError):
+        M.misa_sparse_attention(qi, w, ki, pos, 64, 2, 32, q, k, v, table, k_new=k)
+
+
+def test_a_wait_that_runs_out_is_reported(M):
+    """The tensor-core form with short waits and one key tile never loaded: the call reports the
+    timeout, and the next ones on the same context are right."""
+    c = Case([400 - 9 * i for i in range(40)], Hq=100, Hkv=1, ps=7)
+    assert form(M, c) == "tc"
+    a = [x.cuda() for x in (c.q, c.k, c.v)] + [torch.from_numpy(x).cuda() for x in (c.table, c.pos)]
+    ref = M.misa_paged_attention(*a)
+    assert M.misa_check_device_status("cuda") == 0
+    same = M.misa_testing_paged_attention_wait_expiry(*a, wait_cycles=2_000_000, skip_tile=-1)
+    assert M.misa_check_device_status("cuda") == 0 and torch.equal(same, ref)
+    for tile in (0, 1):
+        M.misa_testing_paged_attention_wait_expiry(*a, wait_cycles=2_000_000, skip_tile=tile)
+        with pytest.raises(M.MisaError) as e:
+            M.misa_check_device_status("cuda")
+        assert e.value.status == 4
+        assert torch.equal(M.misa_paged_attention(*a), ref)
+        assert M.misa_check_device_status("cuda") == 0
+
+
+def test_output_aligned_to_16_bytes_only(M):
+    c = Case([90, 60], Hq=40, Hkv=1, d=64)
+    ref, _ = c.run(M)
+    buf = torch.zeros(ref.numel() + 8, dtype=ref.dtype, device="cuda")
+    out = buf[8:].view(ref.shape)
+    assert out.data_ptr() % 32 == 16
+    c.run(M, out=out)
+    assert torch.equal(out, ref) and bool((buf[:8] == 0).all())
+
+
+def test_compact_a_large_pool(M):
+    """More pages than the plan holds at once per CTA."""
+    rng = np.random.default_rng(9)
+    num, nseq, mp = 400_000, 500, 200
+    perm = rng.permutation(num)[:nseq * mp].reshape(nseq, mp)
+    refs = np.zeros(num, dtype=np.int32)
+    refs[perm] = 1
+    table = perm.astype(np.int32)
+    table[:, 150:] = -1
+    rt, rr, n, _ = po.compact(table.tolist(), refs.tolist())
+    ot, orf, live = M.misa_pages_compact(i32(table), i32(refs))
+    assert M.misa_check_device_status("cuda") == 0 and live.item() == n
+    assert np.array_equal(ot.cpu().numpy(), np.array(rt)) and orf.cpu().tolist() == rr

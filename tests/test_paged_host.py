@@ -20,11 +20,15 @@ def test_workspace_sizes(lib):
     a256 = lambda x: (x + 255) // 256 * 256
     # nseq, T, Hq, Hkv, d, page_size, max_pages, topk.  Partials: two row blocks per CTA (296 at
     # most), of 16 rows, or 32 when more share a head
-    att = lambda rb, d: a256(592 * rb * d * 4) + a256(592 * rb * 8) + a256(296 * 8)
+    att = lambda rb, d, ctas=296: (a256(2 * ctas * rb * d * 4) + a256(2 * ctas * rb * 8)
+                                   + a256(ctas * 8))
     f = c.misa_paged_attention_workspace_size
     assert f(32, 1, 32, 8, 128, 64, 512, 0) == att(16, 128)
     assert f(32, 1, 32, 8, 64, 64, 512, 0) == att(16, 64)
-    assert f(8, 16, 32, 8, 128, 64, 512, 0) == att(32, 128)
+    assert f(8, 4, 32, 8, 128, 64, 512, 0) == att(16, 128)
+    assert f(8, 6, 32, 8, 128, 64, 512, 0) == att(32, 128)
+    # more than 32 rows: the tensor-core form, 148 CTAs of 128 rows
+    assert f(8, 16, 32, 8, 128, 64, 512, 0) == att(128, 128, 148)
     assert f(8, 16, 32, 8, 128, 64, 512, 2048) == att(16, 128)   # each query its own tokens
     assert f(1, 1, 16, 2, 128, 16, 50, 0) == 0                   # a cluster per item: no partials
     for bad in ((0, 1, 32, 8, 128, 64, 512, 0), (1, 0, 32, 8, 128, 64, 512, 0),
@@ -74,6 +78,13 @@ def test_append_refusals(lib, kw, status):
     a.update(kw)
     assert lib.library().misa_paged_append(None, None, None, None, *a.values(), None, None, None,
                                            None) == status
+
+
+def test_wait_probe_refusals(lib):
+    f = lib.library().misa_testing_paged_attention_wait_expiry
+    for wait, skip in ((10, -1), (5_000_000_000, -1), (100000, -2), (100000, 0)):
+        assert f(None, None, None, None, None, None, 0, 2, 1, 8, 2, 128, 16, 16, 4, 0, 0.1, None,
+                 None, None, None, 0, wait, skip, None) == 1
 
 
 def test_upkeep_refusals(lib):
