@@ -44,12 +44,13 @@ struct AttnArgs {
   Divide by_page;  // division by page_size
 };
 
-// Tokens that queries t0 .. t1 of sequence n see, of the longest of their prefixes.
+// Tokens that the longest of the prefixes of queries t0 .. t1 of sequence n holds.  By one thread,
+// eight reads at once, or by a converged warp.
 __device__ __forceinline__ int longest(const AttnArgs& a, int n, int t0, int t1) {
   const int cap = a.max_pages * a.page_size;
   const int32_t* pos = a.pos + (int64_t)n * a.T;
   int last = -1;
-  for (int t = t0; t <= t1; t += 8) {   // eight reads at once
+  for (int t = t0; t <= t1; t += 8) {
     int p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = pos[min(t + i, t1)];
@@ -60,6 +61,13 @@ __device__ __forceinline__ int longest(const AttnArgs& a, int n, int t0, int t1)
     }
   }
   return last + 1;
+}
+__device__ __forceinline__ int longest_warp(const AttnArgs& a, int n, int t0, int t1) {
+  const int cap = a.max_pages * a.page_size;
+  int last = -1;
+  for (int t = t0 + (threadIdx.x & 31); t <= t1; t += 32)
+    last = max(last, last_token(a.pos, (int64_t)n * a.T + t, cap, a.status));
+  return __reduce_max_sync(0xffffffffu, last) + 1;
 }
 
 // An entry is a row block: of a sequence's T * G rows (prefix form, r = t * G + g) or of one
@@ -79,10 +87,10 @@ struct Entry {
       rows = min(RB, a.T * a.G - row0);
     }
   }
-  // tokens the entry walks over
+  // tokens the entry walks over (a converged warp)
   __device__ __forceinline__ int tokens(const AttnArgs& a) const {
     if (SEL) return a.topk;
-    return longest(a, n, row0 / a.G, (row0 + rows - 1) / a.G);
+    return longest_warp(a, n, row0 / a.G, (row0 + rows - 1) / a.G);
   }
 };
 
@@ -136,11 +144,24 @@ struct Range {
   static __device__ __forceinline__ int units_of(int ntok) {
     return max(1, (ntok + UNIT - 1) / UNIT);
   }
-  // Tokens that the entries of group e walk over.
+  // Sequence and queries of the entries of group e (prefix form).
+  struct Queries {
+    int n, t0, t1;
+  };
+  static __device__ __forceinline__ Queries queries_of(const AttnArgs& a, int e) {
+    if (a.side > 1) return {e, 0, a.T - 1};
+    const Entry<RB, SEL> en(a, e);
+    return {en.n, en.row0 / a.G, (en.row0 + en.rows - 1) / a.G};
+  }
+  // Tokens that they walk over (a converged warp).
   static __device__ __forceinline__ int tokens_of(const AttnArgs& a, int e) {
     if (SEL) return a.topk;
-    if (a.side == 1) return Entry<RB, SEL>(a, e).tokens(a);
-    return longest(a, e, 0, a.T - 1);   // all rows of the sequence
+    const Queries q = queries_of(a, e);
+    return longest_warp(a, q.n, q.t0, q.t1);
+  }
+  // Cost of group e.
+  static __device__ __forceinline__ long long cost_of(const AttnArgs& a, int ntok) {
+    return (long long)(kItemCost + units_of(ntok)) * a.Hkv;
   }
 
   // Every thread of the CTA; false: no share.
@@ -156,13 +177,29 @@ struct Range {
       nc = 1;
       return true;
     }
-    const int chunk = (ne + NT - 1) / NT;
-    const int per = SEL ? (kItemCost + units_of(a.topk)) * a.Hkv : 0;   // cost of an entry
-    auto cost_of = [&](int i) { return (kItemCost + units_of(tokens_of(a, i))) * a.Hkv; };
+    const int chunk = (ne + NT - 1) / NT;   // entries of a thread
+    const long long per = SEL ? cost_of(a, a.topk) : 0;
     long long mine = 0, before = 0;
-    total = (long long)ne * per;
+    total = ne * per;
     if (!SEL) {
-      for (int i = tid * chunk; i < min(ne, (tid + 1) * chunk); ++i) mine += cost_of(i);
+      for (int j = 0; j < chunk; ++j) {
+        const int i = tid * chunk + j;
+        Queries q = {0, 0, -1};
+        if (i < ne) q = queries_of(a, i);
+        int ntok = 0;
+        if (a.T <= 8) {
+          if (i < ne) ntok = longest(a, q.n, q.t0, q.t1);
+        } else {   // many queries: the warp takes its lanes' entries one after the other
+          for (uint32_t left = __ballot_sync(0xffffffffu, i < ne); left; left &= left - 1) {
+            const int k = __ffs(left) - 1;
+            const int x = longest_warp(a, __shfl_sync(0xffffffffu, q.n, k),
+                                       __shfl_sync(0xffffffffu, q.t0, k),
+                                       __shfl_sync(0xffffffffu, q.t1, k));
+            if (lane == k) ntok = x;
+          }
+        }
+        if (i < ne) mine += cost_of(a, ntok);
+      }
       long long inc = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -190,7 +227,10 @@ struct Range {
       if (x >= before && x < before + mine) {
         off = x - before;
         e = tid * chunk;
-        for (int n = cost_of(e); off >= n; n = cost_of(e)) {
+        while (chunk > 1) {
+          const Queries q = queries_of(a, e);
+          const long long n = cost_of(a, longest(a, q.n, q.t0, q.t1));
+          if (off < n) break;
           off -= n;
           ++e;
         }
@@ -204,7 +244,7 @@ struct Range {
     return true;
   }
 
-  // The next piece that holds units; false: none.
+  // The next piece that holds units; false: none.  By converged warps.
   __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
     while (x < x1) {
       const int block = blockIdx.x % a.side;
@@ -371,10 +411,15 @@ inline AttnArgs attn_args(const PagedAttn& p, void* scratch, int ctas, int rb, i
 template <typename E, int D, int RB, bool SEL>
 cudaError_t launch_join(AttnArgs a, int ctas, int64_t items, int rows, cudaStream_t st) {
   a.ctas = ctas;
-  const int x = (int)(items < ctas ? items : ctas);   // items that can be split
-  int y = 148 * 8 / x;                                 // blocks of the others' rows: eight an SM
-  if (y > rows) y = rows;
-  return launch_pdl(paged_join_kernel<E, D, RB, SEL>, dim3(x, y > 0 ? y : 1),
+  // Few rows: a block for every CTA and row, most of which end at once.  Many rows: only blocks for
+  // the items that can be split, which find theirs first (about 1 us); eight blocks an SM.
+  int x = ctas, y = rows;
+  if ((int64_t)x * y > 148 * 16) {
+    if (items < ctas) x = (int)items;
+    y = 148 * 8 / x;
+    if (y > rows) y = rows;
+  }
+  return launch_pdl(paged_join_kernel<E, D, RB, SEL>, dim3(x, y),
                     dim3(kJoinTeams * (D / 4)), 0, st, a);
 }
 
