@@ -9,6 +9,7 @@ at import time.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -555,9 +556,12 @@ def _pools(pools, num_pages: int):
             raise ValueError(f"pools[{i}] must be a contiguous CUDA tensor")
         if t.dim() == 0 or t.shape[0] != num_pages:
             raise ValueError(f"pools[{i}] must have {num_pages} pages")
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in pools])
-    sizes = (ctypes.c_int64 * n)(*[t.nbytes // num_pages for t in pools])
-    return ptrs, sizes, n
+    return (array.array("Q", [t.data_ptr() for t in pools]),
+            array.array("q", [t.nbytes // num_pages for t in pools]), n)
+
+
+def _address(a: array.array | None) -> int | None:
+    return None if a is None else a.buffer_info()[0]
 
 
 def misa_pages_resize(page_table, refs, old_len, new_len, page_size: int, pools=(),
@@ -577,8 +581,9 @@ def misa_pages_resize(page_table, refs, old_len, new_len, page_size: int, pools=
     _check("misa_pages_resize",
            _lib.misa_pages_resize(
                page_table.data_ptr(), refs.data_ptr(), old_len.data_ptr(), new_len.data_ptr(),
-               nseq, max_pages, refs.shape[0], page_size, ptrs, sizes, n, out_table.data_ptr(),
-               out_refs.data_ptr(), _STATUS.get(refs.device).data_ptr(), _ptr(ws), nb, _stream()))
+               nseq, max_pages, refs.shape[0], page_size, _address(ptrs), _address(sizes), n,
+               out_table.data_ptr(), out_refs.data_ptr(), _STATUS.get(refs.device).data_ptr(),
+               _ptr(ws), nb, _stream()))
     return out_table, out_refs
 
 
@@ -604,15 +609,15 @@ def misa_pages_compact(page_table, refs, pools=(), out_table=None, out_refs=None
                                           out_refs)
     nseq, max_pages = page_table.shape
     if n_live is None:
-        n_live = torch.empty(1, dtype=torch.int32, device=refs.device)
+        n_live = refs.new_empty(1)
     else:
         _dev(n_live, "n_live", torch.int32)
         _shape(n_live, (1,), "n_live")
     ptrs, sizes, n = _pools(pools, refs.shape[0])
     _check("misa_pages_compact",
            _lib.misa_pages_compact(
-               page_table.data_ptr(), refs.data_ptr(), nseq, max_pages, refs.shape[0], ptrs,
-               sizes, n, out_table.data_ptr(), out_refs.data_ptr(), n_live.data_ptr(),
+               page_table.data_ptr(), refs.data_ptr(), nseq, max_pages, refs.shape[0],
+               _address(ptrs), _address(sizes), n, out_table.data_ptr(), out_refs.data_ptr(), n_live.data_ptr(),
                _STATUS.get(refs.device).data_ptr(), _ptr(ws), nb, _stream()))
     return out_table, out_refs, n_live
 
