@@ -260,9 +260,7 @@ int misa_score_topk_noalloc(const uint16_t* q, const float* w, const uint16_t* k
  * entry is not in [0, num_pages).  Reported and clamped: pos outside [-1, max_pages *
  * page_size).  q, out: dtype, [nseq, T, Hq, d]; lse (nullable) fp32 [nseq, T, Hq].  Sums and
  * softmax statistics are fp32; the weights p are rounded to dtype for their product with v.
- * The values of tokens up to a sequence's last query position must be finite: where one query of
- * a sequence sees a NaN or infinite value, earlier queries of the same call may show it too
- * (keys may be anything, and so may cache rows past the last position).
+ * A NaN or infinite key or value shows in the queries that see it, and in no other.
  * Made for few queries per sequence (decode, drafts): 128 / (Hq / Hkv) queries share one
  * reading of the cache.  ws: misa_paged_attention_workspace_size(...) bytes (0 where few or short items
  * need none, and on invalid arguments; ws may then be NULL).

@@ -54,6 +54,12 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+template <typename O>
+__device__ __forceinline__ O from_f32(float x) { return O(x); }
+
 // c (16 x 8, fp32) += a (16 x 16) * b (16 x 8), operands in the 16-bit type.
 template <typename E>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -103,6 +109,22 @@ __device__ __forceinline__ void cp_async_commit() {
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Sets the elements of a word (two 16-bit values) that are NaN or infinite to 0; true if any was.
+template <typename E>
+__device__ __forceinline__ bool drop_non_finite(uint32_t& x) {
+  constexpr uint32_t kExp = IsBf16<E>::value ? 0x7f80u : 0x7c00u;
+  const bool lo = (x & kExp) == kExp, hi = ((x >> 16) & kExp) == kExp;
+  if (lo) x &= 0xffff0000u;
+  if (hi) x &= 0x0000ffffu;
+  return lo || hi;
+}
+template <typename E>
+__device__ __forceinline__ bool drop_non_finite(uint4& x) {
+  const bool a = drop_non_finite<E>(x.x), b = drop_non_finite<E>(x.y), c = drop_non_finite<E>(x.z),
+             d = drop_non_finite<E>(x.w);
+  return a || b || c || d;
 }
 
 // 2^x; the result's relative error is at most 2^-22.

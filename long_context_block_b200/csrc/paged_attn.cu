@@ -163,7 +163,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
   }
   // last visible token of this thread's rows
   int lim[2 * MT];
-  int lim_min = cap;
+  int lim_min = cap, seen = cap;   // seen: of the rows that see tok0, the least
 #pragma unroll
   for (int i = 0; i < 2 * MT; ++i) {
     const int r = (lane >> 2) + 8 * i;
@@ -171,8 +171,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
     if (!SEL && r < en.rows) {
       lim[i] = last_token(a.pos, (int64_t)en.n * a.T + (en.row0 + r) / a.G, cap, nullptr);
       lim_min = min(lim_min, lim[i]);
+      if (lim[i] >= tok0) seen = min(seen, lim[i]);
     }
   }
+  if (!SEL) seen = __reduce_min_sync(0xffffffffu, seen);
+  bool drop = false;   // NaN or infinite values were left out
   __syncthreads();
 
   float o[MT][DN][4];
@@ -243,6 +246,18 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
     // what a row does not see is -inf
     const int s0 = first + i * UNIT;
     const uint32_t full = KT == 32 ? 0xffffffffu : (1u << KT) - 1u;
+    if (!SEL && min(s0 + KT, tok1) - 1 > seen) {   // values of tokens that some rows do not see
+      for (int r = max(seen + 1 - s0, 0) + lane / CH; r < min(KT, tok1 - s0); r += 32 / CH) {
+        uint4* at = reinterpret_cast<uint4*>(smem + (vt - sm100::smem_u32(smem)) + r * ROWB +
+                                             (((lane % CH) ^ (r & 7)) << 4));
+        uint4 x = *at;
+        if (drop_non_finite<E>(x)) {
+          *at = x;
+          drop = true;
+        }
+      }
+      __syncwarp();
+    }
     if (ok != full || (!SEL && s0 + KT - 1 > lim_min)) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -333,7 +348,19 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
       *reinterpret_cast<float2*>(s_o + (warp * RB + row) * S::OSTR + x * 8 + (lane & 3) * 2) =
           make_float2(o[r >> 1][x][(r & 1) * 2], o[r >> 1][x][(r & 1) * 2 + 1]);
   }
-  __syncthreads();
+  if (SEL) {
+    __syncthreads();
+  } else if (__syncthreads_or(drop)) {
+    const Part at{en.n, en.row0, en.rows, hk, tok0, tok1};
+    for (int r = warp; r < en.rows; r += kWarps) {
+      int w = 0;   // to the part of the largest weights
+      for (int x = 1; x < kWarps; ++x)
+        if (s_ml[x][r].x > s_ml[w][r].x) w = x;
+      if (lane < D / 4)
+        add_non_finite<E, D>(a, at, r, lane * 4, 4, s_o + (w * RB + r) * S::OSTR + lane * 4);
+    }
+    __syncthreads();
+  }
 }
 
 // The CTA's sum over its warps at row r, elements c .. c + 3.
@@ -356,7 +383,8 @@ __device__ __forceinline__ float4 warp_sum(const unsigned char* smem,
 }
 
 template <typename E, int D, int MT, bool SEL>
-__global__ void __launch_bounds__(kThreads, 2) paged_attn_cluster_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 2)
+paged_attn_cluster_kernel(const __grid_constant__ AttnArgs a) {
   using S = Shape<D, MT>;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ float2 s_ml[kWarps][S::RB];
@@ -368,8 +396,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_cluster_kernel(const A
   const Entry<S::RB, SEL> en(a, item / a.Hkv);
   const int ntok = en.tokens(a);
   const int64_t units = (ntok + S::UNIT - 1) / S::UNIT;
-  attend<E, D, MT, SEL>(a, en, hk, (int)(rank * units / size) * S::UNIT,
-                        min(ntok, (int)((rank + 1) * units / size) * S::UNIT), smem, s_ml);
+  const int tok0 = (int)(rank * units / size) * S::UNIT;
+  const int tok1 = min(ntok, (int)((rank + 1) * units / size) * S::UNIT);
+  attend<E, D, MT, SEL>(a, en, hk, tok0, tok1, smem, s_ml);
   float* s_o = reinterpret_cast<float*>(smem);
   const int work = en.rows * (D / 4);
   if (size > 1) {   // this CTA's sum takes the place of its first warp's part
@@ -411,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_cluster_kernel(const A
 }
 
 template <typename E, int D, int MT, bool SEL>
-__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 2)
+paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   using S = Shape<D, MT>;
   constexpr int RB = S::RB, UNIT = S::UNIT;
   using R = Range<RB, SEL, UNIT, kThreads>;
@@ -426,8 +456,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs 
   if (range.cut(a, s_range))
     while (range.next(a, sg)) {
       const Entry<RB, SEL> en(a, sg.e);
-      attend<E, D, MT, SEL>(a, en, sg.hk, sg.uo * UNIT, min(sg.ntok, (sg.uo + sg.take) * UNIT),
-                            smem, s_ml);
+      const int hk = sg.hk, tok0 = sg.uo * UNIT;
+      const int tok1 = min(sg.ntok, (sg.uo + sg.take) * UNIT);
+      attend<E, D, MT, SEL>(a, en, hk, tok0, tok1, smem, s_ml);
       const bool whole = sg.take == sg.units;
       const int slot = 2 * cta + (sg.uo == 0 ? 1 : 0);
       for (int i = threadIdx.x; i < en.rows * (D / 4); i += kThreads) {
@@ -435,14 +466,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const AttnArgs 
         float mm, ll;
         const float4 acc = warp_sum<D, MT>(smem, s_ml, r, c, mm, ll);
         if (whole) {
-          finish<E, D>(a, en.n, en.row0 + r, sg.hk, c, acc, mm, ll);
+          finish<E, D>(a, en.n, en.row0 + r, hk, c, acc, mm, ll);
         } else {
           *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * RB + r) * D + c) = acc;
           if (c == 0) a.part_ml[slot * RB + r] = make_float2(mm, ll);
         }
       }
       __syncthreads();   // the buffers are free for the next segment
-      if (!whole && sg.uo == 0) split = make_int2(sg.e * a.Hkv + sg.hk, sg.last_cta);
+      if (!whole && sg.uo == 0) split = make_int2(sg.e * a.Hkv + hk, sg.last_cta);
     }
   if (threadIdx.x == 0) a.split[cta] = split;
 }

@@ -2,6 +2,7 @@
 // units into equal ranges and the join of partials.
 #pragma once
 
+#include <climits>
 #include <cmath>
 
 #include "internal.h"
@@ -94,6 +95,22 @@ struct Entry {
   }
 };
 
+// Tokens tok0 .. tok1 - 1 of a prefix entry for one key-value head.
+struct Part {
+  int n, row0, rows, hk, tok0, tok1;
+};
+
+// The last token that every row sees, of the rows that see tok0 (what the others gather is never
+// used); with step and at, the least of one thread's share of them.
+__device__ __forceinline__ int seen_by_all(const AttnArgs& a, const Part& p, int step, int at) {
+  int least = INT_MAX;
+  for (int t = p.row0 / a.G + at; t <= (p.row0 + p.rows - 1) / a.G; t += step) {
+    const int last = last_token(a.pos, (int64_t)p.n * a.T + t, a.max_pages * a.page_size, nullptr);
+    if (last >= p.tok0) least = min(least, last);
+  }
+  return least;
+}
+
 // One output position: 4 elements of a row, from its sum of weights and weighted values.
 template <typename E, int D>
 __device__ __forceinline__ void finish(const AttnArgs& a, int n, int rr, int hk, int c,
@@ -119,6 +136,29 @@ __device__ __forceinline__ void add_part(float4& acc, float& ll, float mm, float
   acc.y += x.y * f;
   acc.z += x.z * f;
   acc.w += x.w * f;
+}
+
+// A draft's later tokens lie in the same tiles as those that its earlier queries see, with weight 0
+// for them, but 0 times a NaN or infinite value is NaN.  So such values of tokens that not every
+// row of the block sees are set to 0 in shared memory, and this adds them, from the cache, to the
+// elements c .. c + n - 1 (at `to`) of a row that sees them: a weight is positive, and any positive
+// weight gives the same sum.  Not inlined, as its code slows down short calls: 0.5 us of 10 us.
+template <typename E, int D, typename O>
+__device__ __noinline__ void add_non_finite(const AttnArgs& a, Part p, int r, int c, int n, O* to) {
+  const int cap = a.max_pages * a.page_size;
+  const int last = min(p.tok1 - 1, last_token(a.pos, (int64_t)p.n * a.T + (p.row0 + r) / a.G, cap,
+                                              nullptr));
+  if (last < p.tok0) return;
+  for (int s = seen_by_all(a, p, 1, 0) + 1; s <= last; ++s) {
+    const int row = cache_row(a.table + (int64_t)p.n * a.max_pages, s, a.page_size, a.by_page,
+                              a.num_pages, nullptr);
+    if (row < 0) continue;
+    const E* v = static_cast<const E*>(a.v) + ((int64_t)row * a.Hkv + p.hk) * D + c;
+    for (int i = 0; i < n; ++i) {
+      const float x = to_f32(v[i]);
+      if (!isfinite(x)) to[i] = from_f32<O>(to_f32(to[i]) + x);
+    }
+  }
 }
 
 // The share of one CTA of NT threads in all items' units.  An item of u units costs kItemCost + u:

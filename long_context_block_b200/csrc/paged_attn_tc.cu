@@ -171,7 +171,8 @@ __device__ __forceinline__ void store32(void* to, const uint32_t* v) {
 constexpr float kSlack = 8.f;
 
 template <typename E, int D, bool SEL>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
   using C = Cfg<D>;
   using R = Range<kRows, SEL, kTile, kThreads>;
   extern __shared__ unsigned char smem_raw[];
@@ -179,6 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ float2 s_ml[2][2][kRows];   // [segment parity][group][row]
+  __shared__ int s_non_finite;           // a value that not every row sees was NaN or infinite and
+                                         // left out, in this segment or one before
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
   volatile int* abort_flag = &s_abort;
 
   if (tid == 0) {
-    s_abort = 0;
+    s_abort = s_non_finite = 0;
     for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(&kfull[i], 32 * kLoadWarps / 2);
       mbar_init(&kfree[i], 1);
@@ -405,6 +408,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
               store32(out + x, reinterpret_cast<const uint32_t*>(o + x));
           }
         }
+        if (!SEL && mine && n > 0 && *static_cast<volatile int*>(&s_non_finite)) {
+          const int c = group * (D / 2);
+          const Part at{en.n, en.row0, en.rows, sg.hk, tok0, tok1};
+          if (whole)
+            add_non_finite<E, D>(a, at, row, c, D / 2, static_cast<E*>(a.out) + head * D + c);
+          else
+            add_non_finite<E, D>(a, at, row, c, D / 2,
+                                 a.part_o + ((int64_t)slot * kRows + row) * D + c);
+        }
         if (mine && group == 0) {
           if (!whole)
             a.part_ml[slot * kRows + row] = make_float2(m, l);
@@ -539,12 +551,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const AttnAr
       const int tok0 = sg.uo * kTile, tok1 = min(sg.ntok, (sg.uo + sg.take) * kTile);
       const int n = (tok1 - tok0 + kTile - 1) / kTile;
       if (n == 0) continue;
+      const Entry<kRows, SEL> en(a, sg.e);
+      int seen = INT_MAX;
+      if (!SEL)
+        seen = seen_by_all(a, {en.n, en.row0, en.rows, sg.hk, tok0, tok1}, 32, lane);
       if (!(ok = warp_wait(qfull, seg))) break;
       if (!(ok = scores(g)) || (n > 1 && !(ok = scores(g + 1)))) break;
       if (seg > 0 && !(ok = warp_wait(ofree, seg - 1))) break;
+      if (!SEL) seen = __reduce_min_sync(0xffffffffu, seen);
       for (int i = 0; i < n; ++i) {
         const int gi = g + i, st = gi % C::kVStages, buf = gi & 1;
         if (!(ok = warp_wait(&vfull[st], gi / C::kVStages))) break;
+        const int s0 = tok0 + i * kTile, s1 = min(s0 + kTile, tok1);
+        // Values of tokens that some rows do not see, before the product reads them.  Here, as this
+        // warp waits for them anyway: a loader that looked at its own copies stood still until
+        // they had landed (70 us instead of 65 us for 32 sequences of 16 x 4 rows, 8 key-value
+        // heads, 1024 tokens), and the warps of the weights took 67 us.
+        if (!SEL && s1 - 1 > seen) {
+          unsigned char* tile = smem + C::kV + st * C::kTileBytes;
+          bool drop = false;
+          for (int x = max(seen + 1 - s0, 0) * (D / 8) + lane; x < (s1 - s0) * (D / 8); x += 32) {
+            const int r = x / (D / 8), c = x % (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * C::kHalf + r * 128 +
+                                                 (((c & 7) ^ (r & 7)) << 4));
+            uint4 y = *at;
+            if (drop_non_finite<E>(y)) {
+              *at = y;
+              drop = true;
+            }
+          }
+          if (drop) s_non_finite = 1;
+          __threadfence_block();
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
         const uint64_t v = v0 + st * (C::kTileBytes >> 4);
         // The groups' weights are waited for apart: of two warps on a scheduler one is ahead by
         // its exponentials, and so one computes while the other waits.

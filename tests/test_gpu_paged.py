@@ -269,6 +269,50 @@ def test_infinite_scores_and_values(M):
     assert bool(bad[:, 7].all()) and not bool(bad[:, :7].any()) and not bool(bad[:, 8:].any())
 
 
+@pytest.mark.parametrize("name", [
+    "draft4", "draft16", "draft7_d64", "ranges_draft4_d64", "rows_draft16_group8",
+    "tc_one_tile_d64_fp16", "tc_whole_items_draft", "tc_ranges_fp16_draft", "tc_long_one",
+    "tc_two_blocks_side_by_side", "tc_many_blocks"])
+def test_values_that_only_some_queries_see(M, name):
+    """NaN and infinite values show in the queries that see them, and in no other of the same
+    call: with each set to 0 the rest is the same to the bit."""
+    c = Case(**CASES[name], poison=False)
+    T, rng = c.T, np.random.default_rng(5)
+    for n, x in enumerate(c.lens):      # some queries shorter by far than the rest, or padded
+        if x > 200 and n % 2:
+            c.pos[n, 0] = x // 3
+            c.pos[n, 1] = -1
+    H, d = c.k.shape[2:]
+    special = [float("nan"), float("inf"), -float("inf")]
+    marks = []
+    for n, x in enumerate(c.lens):
+        for _ in range(6):
+            s = int(x - 1 - rng.integers(0, T))
+            if s < 0:
+                continue
+            row = (c.table[n, s // c.ps], s % c.ps, int(rng.integers(H)), int(rng.integers(d)))
+            marks.append((n, s, row, special[int(rng.integers(3))]))
+    for _, _, row, _ in marks:
+        c.v[row] = 0
+    ref, lse = c.run(M)
+    c.check(ref, lse)
+    want = ref.float().cpu()
+    last = {(n, row): x for n, s, row, x in marks}     # the value that a place ends with
+    where = {(n, row): s for n, s, row, x in marks}
+    G = c.q.shape[2] // H
+    for (n, row), x in last.items():
+        c.v[row] = x
+        for t in range(T):
+            if c.pos[n, t] >= where[n, row]:
+                want[n, t, row[2] * G:(row[2] + 1) * G, row[3]] += x
+    out, lse2 = c.run(M)
+    assert M.misa_check_device_status(out.device) == 0
+    assert torch.equal(lse, lse2)
+    assert torch.equal(torch.nan_to_num(out.float().cpu(), 7.0, 8.0, 9.0),
+                       torch.nan_to_num(want, 7.0, 8.0, 9.0))
+    assert not torch.isfinite(want).all() and torch.isfinite(want).float().mean() > 0.5
+
+
 def test_a_repeated_token_counts_twice(M):
     c = Case([50], topk=4, poison=False)
     c.idx[0, 0] = [7, 3, 7, 7]
