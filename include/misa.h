@@ -258,8 +258,8 @@ int misa_score_topk_noalloc(const uint16_t* q, const float* w, const uint16_t* k
  * -inf) gets out 0 and lse -inf; cache rows that no query sees are not read, so they may hold
  * anything.  Reported and skipped: idx entries outside their query's prefix, tokens whose page
  * entry is not in [0, num_pages).  Reported and clamped: pos outside [-1, max_pages *
- * page_size).  q, out: dtype, [nseq, T, Hq, d]; lse (nullable) fp32 [nseq, T, Hq].  Sums and
- * softmax statistics are fp32; the weights p are rounded to dtype for their product with v.
+ * page_size).  q, out: dtype, [nseq, T, Hq, d]; lse (nullable) fp32 [nseq, T, Hq].  out may be
+ * q itself; otherwise out and lse must not overlap one another, q or the caches.  Sums and softmax statistics are fp32; the weights p are rounded to dtype for their product with v.
  * A NaN or infinite key or value shows in the queries that see it, and in no other.
  * Made for few queries per sequence (decode, drafts): 128 / (Hq / Hkv) queries share one
  * reading of the cache.  ws: misa_paged_attention_workspace_size(...) bytes (0 where few or short items
@@ -281,6 +281,7 @@ int misa_paged_attention(const void* q, const void* k_cache, const void* v_cache
  * (with two for one, which of them each 16 bytes come from is undefined), and a page that others
  * hold too is theirs as well: misa_pages_resize copies it first.  Reported and skipped: pos
  * outside [-1, max_pages * page_size), page entries outside [0, num_pages).  No workspace.
+ * k_cache and v_cache must not overlap, and no row written may be one of k_new or v_new.
  */
 int misa_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
                       const int32_t* page_table, int dtype, int nseq, int T, int Hkv, int d,

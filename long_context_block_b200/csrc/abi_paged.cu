@@ -55,11 +55,15 @@ int check_scratch(void* ws, size_t ws_bytes, size_t need) {
   return check_dev(ws, need, 256);
 }
 
+// What is written must not overlap what another buffer holds.
+int check_apart(const void* x, size_t xb, const void* y, size_t yb) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a < b + yb && b < a + xb ? MISA_ERR_INVALID_ARG : MISA_OK;
+}
+
 // out may be the input itself, but must not overlap it otherwise.
 int check_out(const void* in, const void* out, size_t bytes) {
-  if (in == out) return MISA_OK;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
-  return a < b + bytes && b < a + bytes ? MISA_ERR_INVALID_ARG : MISA_OK;
+  return in == out ? MISA_OK : check_apart(in, bytes, out, bytes);
 }
 
 int check_upkeep(int op, const int32_t* table, const int32_t* refs, int nseq, int max_pages,
@@ -131,6 +135,16 @@ static int paged_attention(const void* q, const void* k_cache, const void* v_cac
   MISA_TRY(check_dev(out, rows * Hq * d * 2, 16));
   MISA_TRY(check_opt(lse, rows * Hq * 4, 4));
   MISA_TRY(check_opt(device_status, 4, 4));
+  const size_t ob = rows * Hq * d * 2, lb = rows * Hq * 4;
+  MISA_TRY(check_out(q, out, ob));
+  MISA_TRY(check_apart(out, ob, k_cache, pool));
+  MISA_TRY(check_apart(out, ob, v_cache, pool));
+  if (lse) {
+    MISA_TRY(check_apart(lse, lb, out, ob));
+    MISA_TRY(check_apart(lse, lb, q, ob));
+    MISA_TRY(check_apart(lse, lb, k_cache, pool));
+    MISA_TRY(check_apart(lse, lb, v_cache, pool));
+  }
   PagedAttn p = {q,    k_cache, v_cache, page_table, pos, idx,       out,       lse,       dtype,
                  nseq, T,       Hq,      Hkv,        d,   num_pages, page_size, max_pages, topk,
                  scale, probe};
@@ -179,6 +193,7 @@ int misa_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
   MISA_TRY(check_dev(page_table, (size_t)nseq * max_pages * 4, 4));
   MISA_TRY(check_dev(k_cache, pool, 16));
   MISA_TRY(check_dev(v_cache, pool, 16));
+  MISA_TRY(check_apart(k_cache, pool, v_cache, pool));
   MISA_TRY(check_opt(device_status, 4, 4));
   return cuda_status(launch_paged_append(k_new, v_new, pos, page_table, nseq, T, Hkv * d * 2,
                                          num_pages, page_size, max_pages, k_cache, v_cache,

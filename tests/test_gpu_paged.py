@@ -468,6 +468,49 @@ def test_misaligned_and_short_buffers_are_refused(M):
     assert rc == 5
 
 
+@pytest.mark.parametrize("name", ["draft4", "rows33", "ranges_draft4_d64", "ranges_sel",
+                                  "tc_whole_items_draft", "tc_ranges", "tc_sel_ranges",
+                                  "tc_two_blocks_side_by_side"])
+def test_output_over_the_queries(M, name):
+    c = Case(**CASES[name])
+    ref, lse = c.run(M)
+    q, k, v = (x.cuda() for x in (c.q, c.k, c.v))
+    idx = None if c.idx is None else torch.from_numpy(c.idx).cuda()
+    out, l2 = M.misa_paged_attention(q, k, v, torch.from_numpy(c.table).cuda(),
+                                     torch.from_numpy(c.pos).cuda(), idx=idx, scale=c.scale,
+                                     return_lse=True, out=q)
+    assert out is q and torch.equal(out, ref) and torch.equal(l2, lse)
+
+
+def test_overlapping_buffers_are_refused(M):
+    c = Case([40], Hq=4)
+    buf = torch.zeros(3, c.k.shape[0] // 2, *c.k.shape[1:], dtype=c.k.dtype, device="cuda")
+    half = buf.shape[1] * buf[0, 0].numel()
+    k, v = buf[:2].view(c.k.shape), buf[1:].view(c.k.shape)     # v starts in the middle of k
+    q = c.q.cuda()
+    table, pos = torch.from_numpy(c.table).cuda(), torch.from_numpy(c.pos).cuda()
+    new = torch.zeros(1, 1, *c.k.shape[2:], dtype=c.k.dtype, device="cuda")
+    assert half and c.k.shape[0] % 2 == 0
+
+    def refused(call):
+        with pytest.raises(M.MisaError) as e:
+            call()
+        assert e.value.status == 1
+
+    refused(lambda: M.misa_paged_append(new, new, pos, table, k, v))
+    refused(lambda: M.misa_paged_append(new, new, pos, table, k, k))
+    inside = buf.view(-1)[:q.numel()].view(q.shape)
+    refused(lambda: M.misa_paged_attention(q, k, v, table, pos, out=inside))
+    two = torch.zeros(2 * q.numel(), dtype=q.dtype, device="cuda")
+    shifted = two[8:8 + q.numel()].view(q.shape)
+    refused(lambda: M.misa_paged_attention(two[:q.numel()].view(q.shape), k, v, table, pos,
+                                           out=shifted))
+    lse = two.view(torch.float32)[:4].view(1, 1, 4)
+    refused(lambda: M.misa_paged_attention(q, k, v, table, pos, out=two[:q.numel()].view(q.shape),
+                                           lse=lse))
+    M.misa_paged_attention(q, k, v, table, pos)                # two readings may overlap
+
+
 # ------------------------------------------------------------------------------------- append
 
 APPENDS = {
