@@ -439,7 +439,7 @@ def _scratch(nbytes: int, like: torch.Tensor):
 
 
 def _shape(t: torch.Tensor, shape: tuple, name: str):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
