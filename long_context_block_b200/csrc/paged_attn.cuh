@@ -169,17 +169,19 @@ __device__ __noinline__ void add_non_finite(const AttnArgs& a, Part p, int r, in
 // own).
 template <int RB, bool SEL, int UNIT, int NT>
 struct Range {
-  long long x, x1, total, off;   // position, end, sum of all costs; from the start of item e to x
-  int e, nc;                     // e: counts entries, or groups of a.side entries
+  long long x, x1, total;   // position, end, sum of all costs
+  int e, hk, at, nc;        // e: counts entries, or groups of a.side entries; at: from the start of
+                            // the item (e, hk) to x
+  int ntok;                 // tokens of e; -1: not looked up yet
 
   struct Shared {
     long long sum[NT / 32], off;
-    int e, ntok[NT];
+    int e, first, ntok[NT];
   };
   // A piece of one item: units uo .. uo + take - 1 of `units`.
   struct Segment {
     int e, hk, uo, take, units, ntok;
-    int last_cta;   // of the item
+    int last_cta;   // of an item that starts here and ends in another CTA
   };
 
   static __device__ __forceinline__ int units_of(int ntok) {
@@ -212,15 +214,18 @@ struct Range {
     if (a.whole) {   // gridDim.x = side * entries * Hkv
       const int item = blockIdx.x / a.side;
       e = item / a.Hkv;
-      total = x1 = kItemCost + units_of(tokens_of(a, e));
-      off = (item - e * a.Hkv) * x1;
+      ntok = tokens_of(a, e);
+      total = x1 = kItemCost + units_of(ntok);
+      hk = item - e * a.Hkv;
+      at = 0;
       x = 0;
       nc = 1;
       return true;
     }
     const int chunk = (ne + NT - 1) / NT;   // entries of a thread
     const long long per = SEL ? cost_of(a, a.topk) : 0;
-    long long mine = 0, before = 0;
+    long long mine = 0, before = 0, off;
+    int tokens = 0;   // of this thread's last entry
     total = ne * per;
     if (!SEL) {
       // With few queries a thread reads its entries' positions, eight at once; with many the
@@ -233,7 +238,8 @@ struct Range {
         if (alone) {
           if (i < ne) {
             const Queries q = queries_of(a, i);
-            mine += cost_of(a, longest(a, q.n, q.t0, q.t1));
+            tokens = longest(a, q.n, q.t0, q.t1);
+            mine += cost_of(a, tokens);
           }
           continue;
         }
@@ -269,7 +275,8 @@ struct Range {
           }
         }
         __syncthreads();
-        if (i < ne) mine += cost_of(a, sh.ntok[tid]);
+        tokens = sh.ntok[tid];
+        if (i < ne) mine += cost_of(a, tokens);
         __syncthreads();
       }
       long long inc = mine;
@@ -295,24 +302,31 @@ struct Range {
     if constexpr (SEL) {
       e = (int)(x / per);
       off = x - (long long)e * per;
+      ntok = a.topk;
     } else {
       if (x >= before && x < before + mine) {
         off = x - before;
         e = tid * chunk;
         while (chunk > 1) {
           const Queries q = queries_of(a, e);
-          const long long n = cost_of(a, longest(a, q.n, q.t0, q.t1));
+          tokens = longest(a, q.n, q.t0, q.t1);
+          const long long n = cost_of(a, tokens);
           if (off < n) break;
           off -= n;
           ++e;
         }
         sh.e = e;
         sh.off = off;
+        sh.first = tokens;
       }
       __syncthreads();
       e = sh.e;
       off = sh.off;
+      ntok = sh.first;
     }
+    const int cost = kItemCost + units_of(ntok);
+    hk = (int)(off / cost);
+    at = (int)(off - (long long)hk * cost);
     return true;
   }
 
@@ -320,22 +334,27 @@ struct Range {
   __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
     while (x < x1) {
       const int block = blockIdx.x % a.side;
+      if (ntok < 0) ntok = tokens_of(a, e);
       s.e = e * a.side + block;
-      s.ntok = tokens_of(a, e);
-      s.units = units_of(s.ntok);
-      const int cost = kItemCost + s.units;
-      s.hk = (int)(off / cost);
-      const int at = (int)(off - (long long)s.hk * cost);
-      const int go = (int)min((long long)(cost - at), x1 - x);
+      s.hk = hk;
+      s.ntok = ntok;
+      s.units = units_of(ntok);
+      const int cost = kItemCost + s.units, go = (int)min((long long)(cost - at), x1 - x);
       s.uo = max(0, at - kItemCost);
       s.take = max(0, at + go - kItemCost) - s.uo;
+      s.last_cta = 0;
       // position y of all costs lies in group floor(((y + 1) nc - 1) / total); y: the last unit
-      s.last_cta = (int)(((x - at + cost) * nc - 1) / total) * a.side + block;
+      if (s.uo == 0 && at + go < cost)
+        s.last_cta = (int)(((x - at + cost) * nc - 1) / total) * a.side + block;
       x += go;
-      off += go;
-      if (off == (long long)cost * a.Hkv) {
-        ++e;
-        off = 0;
+      at += go;
+      if (at == cost) {
+        at = 0;
+        if (++hk == a.Hkv) {
+          hk = 0;
+          ++e;
+          if (!SEL) ntok = -1;
+        }
       }
       if (s.take > 0) return true;
     }

@@ -11,7 +11,8 @@
 //                 that nothing is exchanged in between; two score buffers keep the next tile's
 //                 scores ready
 //   warps 8, 9 and 10, 11   gather the tiles of keys and of values: page entries, then 16-byte
-//                 asynchronous copies into the 128-byte-swizzled operand layout
+//                 asynchronous copies into the 128-byte-swizzled operand layout; the warps of the
+//                 values also fetch the queries, but those of the first segment
 //   warp 12       one thread issues the products S = Q K^T and O += P V, fp32 sums in tensor memory
 // A group's maximum moves only when a row's scores exceed it by more than 2^8, so that O, which
 // stays in tensor memory, is rescaled a few times per item at most; any reference gives the same
@@ -54,9 +55,9 @@ struct Cfg {
   static constexpr int kQ = kV + kVStages * kTileBytes;
   static constexpr int kLive = kQ + kTileBytes;          // [kLiveDepth][4] words
   static constexpr int kBars = kLive + kLiveDepth * 16;
-  // kfull, kfree [kKStages], vfull, vfree [kVStages], sfull [2], pfull [2][2], qfull, odone,
-  // joined, ofree, drain, live [kLiveDepth]
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 6 + 5 + kLiveDepth;
+  // kfull, kfree [kKStages], vfull, vfree [kVStages], sfull [2], pfull [2][2], qfirst, qfull, qfree,
+  // odone, joined, ofree, drain, live [kLiveDepth]
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 6 + 7 + kLiveDepth;
   static constexpr int kBytes = kBars + kNumBars * 8 + 1024;   // 1 KB alignment of the base
   static_assert(kBytes <= 224 * 1024, "shared memory");
 };
@@ -187,7 +188,7 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
   uint64_t *kfull = bars, *kfree = kfull + C::kKStages, *vfull = kfree + C::kKStages,
            *vfree = vfull + C::kVStages, *sfull = vfree + C::kVStages, *pfull = sfull + 2,
-           *qfull = pfull + 4, *odone = qfull + 1, *joined = odone + 1, *ofree = joined + 1,
+           *qfirst = pfull + 4, *qfull = qfirst + 1, *qfree = qfull + 1, *odone = qfree + 1, *joined = odone + 1, *ofree = joined + 1,
            *drain = ofree + 1, *live = drain + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   volatile int* abort_flag = &s_abort;
@@ -204,7 +205,9 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
     }
     for (int i = 0; i < 2; ++i) mbar_init(&sfull[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&pfull[i], 32 * kSoftWarps / 2);
-    mbar_init(qfull, 32 * kSoftWarps);
+    mbar_init(qfirst, 32 * kSoftWarps);
+    mbar_init(qfull, 32 * kLoadWarps / 2);
+    mbar_init(qfree, 1);
     mbar_init(odone, 1);
     mbar_init(joined, 32 * kSoftWarps);
     mbar_init(ofree, 32 * kSoftWarps);
@@ -242,6 +245,13 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
     }
     return true;
   };
+  auto scaled = [&](uint4 x) {   // a query's elements, with the scale's sign
+    x.x = (x.x ^ a.q_flip) & a.q_keep;
+    x.y = (x.y ^ a.q_flip) & a.q_keep;
+    x.z = (x.z ^ a.q_flip) & a.q_keep;
+    x.w = (x.w ^ a.q_flip) & a.q_keep;
+    return x;
+  };
   int g = 0;        // tiles before this segment, in every role
   int seg = 0;      // segments with tiles before this one
   bool ok = true;
@@ -258,27 +268,23 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
       const bool mine = row < en.rows, warp_live = warp % 4 * 32 < en.rows;
       const int rr = en.row0 + row, t = mine ? rr / a.G : 0;
       float m = -INFINITY, l = 0.f;
-      if (n > 0) {
-        // half of the row of Q; the products of the segment before have ended
+      if (n > 0 && seg == 0) {   // half of the row of Q; of later segments a loader does it
         const uint4* q = reinterpret_cast<const uint4*>(
             static_cast<const E*>(a.q) +
             (((int64_t)en.n * a.T + t) * a.Hq + sg.hk * a.G + (rr - t * a.G)) * D);
         unsigned char* dst = smem + C::kQ + row * 128;
+        uint4 x[D / 16];
 #pragma unroll
-        for (int c0 = 0; c0 < D / 16; ++c0) {
-          const int c = group * (D / 16) + c0;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (mine) {
-            x = q[c];
-            x.x = (x.x ^ a.q_flip) & a.q_keep;
-            x.y = (x.y ^ a.q_flip) & a.q_keep;
-            x.z = (x.z ^ a.q_flip) & a.q_keep;
-            x.w = (x.w ^ a.q_flip) & a.q_keep;
-          }
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kHalf + (((c & 7) ^ (row & 7)) << 4)) = x;
+        for (int i = 0; i < D / 16; ++i)
+          x[i] = mine ? q[group * (D / 16) + i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int c = group * (D / 16) + i;
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kHalf + (((c & 7) ^ (row & 7)) << 4)) =
+              scaled(x[i]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(qfull);
+        mbar_arrive(qfirst);
       }
       int lim = INT_MAX;
       if (!SEL && mine)
@@ -477,6 +483,42 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
       if (SEL) last_sel = last_token(a.pos, sel_row, cap, a.status);
 #pragma unroll
       for (int x = 0; x < 2; ++x) page_of(tok[x], page[x], in_page[x]);
+      if (vals && n > 0 && seg > 0) {
+        // The query rows, as soon as the last scores of the segment before are there: their
+        // weights, their product and the output follow meanwhile.  From the output to the next
+        // scores 1.5 to 2 us; 5.5 us when the warps of the weights loaded them after the output.
+        // (By the warps of the keys they held up the next keys.)
+        if (!(ok = warp_wait(qfree, seg - 1))) break;
+        int row[2];   // of the two rows that a lane looks up
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = w * 64 + x * 32 + lane, rr = en.row0 + r, t = rr / a.G;
+          row[x] = r < en.rows ? t * a.Hq + (rr - t * a.G) : -1;
+        }
+        const char* q = static_cast<const char*>(a.q) +
+                        ((int64_t)en.n * a.T * a.Hq + sg.hk * a.G) * (D * 2) + c * 16;
+        const uint32_t dst = smem_u32(smem) + C::kQ + (c >> 3) * C::kHalf;
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+          const int in = j * PER + lane / CH, r = w * 64 + in;
+          const int x = __shfl_sync(0xffffffffu, row[j * PER / 32], in & 31);
+          cp_async16_or_zero(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                             q + (int64_t)max(x, 0) * (D * 2), x >= 0);
+        }
+        if (a.q_flip != 0 || a.q_keep != 0xffffffffu) {   // a scale below zero, or zero
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          for (int j = 0; j < STEPS; ++j) {
+            const int r = w * 64 + j * PER + lane / CH;
+            uint4* at = reinterpret_cast<uint4*>(smem + C::kQ + (c >> 3) * C::kHalf + r * 128 +
+                                                 (((c & 7) ^ (r & 7)) << 4));
+            *at = scaled(*at);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(qfull);
+        } else {
+          cp_async_mbar_arrive(qfull);
+        }
+      }
       for (int i = 0; i < n; ++i) {
         const int gi = g + i;
         int src[2];
@@ -518,6 +560,7 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
       g += n;
+      if (n > 0) ++seg;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");   // this CTA's copies land before it ends
   } else {
@@ -529,7 +572,7 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
     const uint32_t smem0 = smem_u32(smem);
     const uint64_t q0 = desc_kmajor_sw128(smem0 + C::kQ), k0 = desc_kmajor_sw128(smem0 + C::kK),
                    v0 = desc_mnmajor_sw128(smem0 + C::kV, C::kHalf);
-    auto scores = [&](int gi) {
+    auto scores = [&](int gi, bool last) {
       const int st = gi % C::kKStages, buf = gi & 1;
       if (!warp_wait(&kfull[st], gi / C::kKStages)) return false;
       tc_fence_after();
@@ -543,6 +586,7 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
         }
         mma_commit(&kfree[st]);
         mma_commit(&sfull[buf]);
+        if (last) mma_commit(qfree);
       }
       __syncwarp();
       return true;
@@ -555,8 +599,8 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
       int seen = INT_MAX;
       if (!SEL)
         seen = seen_by_all(a, {en.n, en.row0, en.rows, sg.hk, tok0, tok1}, 32, lane);
-      if (!(ok = warp_wait(qfull, seg))) break;
-      if (!(ok = scores(g)) || (n > 1 && !(ok = scores(g + 1)))) break;
+      if (!(ok = seg == 0 ? warp_wait(qfirst, 0) : warp_wait(qfull, seg - 1))) break;
+      if (!(ok = scores(g, n == 1)) || (n > 1 && !(ok = scores(g + 1, n == 2)))) break;
       if (seg > 0 && !(ok = warp_wait(ofree, seg - 1))) break;
       if (!SEL) seen = __reduce_min_sync(0xffffffffu, seen);
       for (int i = 0; i < n; ++i) {
@@ -606,7 +650,7 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
           __syncwarp();
         }
         if (!ok) break;
-        if (i + 2 < n && !(ok = scores(gi + 2))) break;   // over the weights just used
+        if (i + 2 < n && !(ok = scores(gi + 2, i + 3 == n))) break;   // over the weights just used
       }
       if (!ok) break;
       g += n;
