@@ -509,21 +509,25 @@ int cluster_size(const PagedAttn& p) {
 
 // Whether the tensor-core form (paged_attn_tc.cu) runs: for more rows on a token than a warp
 // holds, but for little work the clusters of this file are quicker, as they need no join.  Measured
-// at 64 rows (16 drafted queries, groups of 4): one sequence of 1024 tokens, 8 key-value heads, 11.9
-// against 17.0 us, 8 sequences of 1024 (2048 units) 23.2 against 28.5 us, of 4096 66.6 against 46.5
-// us, 32 sequences of 4096 188 against 112 us.  Up to four tiles an item stays with one CTA, without
-// a join, and 512 units are enough: 8 sequences of 256 tokens 13.5 against 11.6 us.
+// at 64 rows, clusters against tensor cores.  Units of a cluster's CTA: 4 (32 sequences of 1024
+// tokens, one key-value head) 15.3 against 18.2 us, (8 x 2048 selected tokens) 13.6 against 14.5 us;
+// 8 (one sequence of 4096 tokens, 8 key-value heads) 19.9 against 16.4 us, (32 x 2048 selected)
+// 21.5 against 19.7 us, (8 sequences of 1024 tokens, 8 heads) 23.5 against 23.8 us.  Units in all:
+// 8192 (8 sequences of 4096 tokens, 8 heads) 66.6 against 39.2 us.  Up to four tiles an item stays
+// with one CTA, without a join, and 512 units are enough: 8 sequences of 256 tokens 15.6 against
+// 11.6 us.
 bool use_tc(const PagedAttn& p) {
   const int rows = attn_rows(p);
   if (rows <= 32) return false;
   const int64_t heads = (int64_t)p.nseq * (p.topk > 0 ? p.T : 1) * p.Hkv;
   const int64_t span = p.topk > 0 ? p.topk : (int64_t)p.max_pages * p.page_size;
   const int64_t unit = kWarps * (2048 / p.d);
-  const int64_t work = heads * ((rows + 31) / 32) * ((span + unit - 1) / unit);
+  const int64_t units = (span + unit - 1) / unit, work = heads * ((rows + 31) / 32) * units;
   const int64_t tiles = (span + 127) / 128;
   if (tiles == 1) return true;
   if (tiles <= 4 && heads * ((rows + 127) / 128) <= 148) return work >= 512;
-  return work > 2048 || cluster_size(p) == 0;
+  const int c = cluster_size(p);
+  return c == 0 || work > 2048 || (units + c - 1) / c >= 8;
 }
 
 template <typename E, int D, int MT, bool SEL>
