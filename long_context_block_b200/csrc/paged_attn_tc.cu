@@ -188,8 +188,8 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
   uint64_t *kfull = bars, *kfree = kfull + C::kKStages, *vfull = kfree + C::kKStages,
            *vfree = vfull + C::kVStages, *sfull = vfree + C::kVStages, *pfull = sfull + 2,
-           *qfirst = pfull + 4, *qfull = qfirst + 1, *qfree = qfull + 1, *odone = qfree + 1, *joined = odone + 1, *ofree = joined + 1,
-           *drain = ofree + 1, *live = drain + 1;
+           *qfirst = pfull + 4, *qfull = qfirst + 1, *qfree = qfull + 1, *odone = qfree + 1,
+           *joined = odone + 1, *ofree = joined + 1, *drain = ofree + 1, *live = drain + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   volatile int* abort_flag = &s_abort;
 

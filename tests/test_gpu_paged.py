@@ -188,6 +188,18 @@ CASES = {
     "tc_sel_ranges_d64_two_blocks": dict(lens=[2500] * 20, T=3, topk=1000, Hq=160, Hkv=1, d=64,
                                          dtype="fp16"),
     "tc_negative_scale": dict(lens=[100], spare_slots=0, Hq=48, Hkv=1, scale=-0.15),
+    # several items to a CTA, some of no tokens
+    "tc_many_items": dict(lens=[(i * 37) % 260 for i in range(500)], Hq=40, Hkv=1),
+    "tc_many_items_negative_scale": dict(lens=[(i * 37) % 260 for i in range(500)], Hq=40, Hkv=1,
+                                         d=64, scale=-0.15),
+    "tc_many_items_zero_scale": dict(lens=[(i * 61) % 300 for i in range(400)], Hq=50, Hkv=1,
+                                     dtype="fp16", scale=0.0),
+    "tc_many_items_draft": dict(lens=[(i * 83) % 250 for i in range(430)], T=10, Hq=8, Hkv=2, d=64,
+                                ps=7),
+    "tc_many_items_chunk": dict(lens=[(i * 83) % 250 for i in range(430)], T=40, Hq=1, Hkv=1, d=64,
+                                ps=7),
+    "tc_many_items_sel": dict(lens=[100 + i for i in range(180)], topk=300, Hq=80, Hkv=2, d=64,
+                              ps=32, scale=-0.1),
     "tc_zero_scale": dict(lens=[100], spare_slots=0, Hq=48, Hkv=1, scale=0.0),
     "negative_scale": dict(lens=[300], scale=-0.2),
     "zero_scale": dict(lens=[100], scale=0.0),
@@ -272,7 +284,7 @@ def test_infinite_scores_and_values(M):
 @pytest.mark.parametrize("name", [
     "draft4", "draft16", "draft7_d64", "ranges_draft4_d64", "rows_draft16_group8",
     "tc_one_tile_d64_fp16", "tc_whole_items_draft", "tc_ranges_fp16_draft", "tc_long_one",
-    "tc_two_blocks_side_by_side", "tc_many_blocks"])
+    "tc_two_blocks_side_by_side", "tc_many_blocks", "tc_many_items_draft"])
 def test_values_that_only_some_queries_see(M, name):
     """NaN and infinite values show in the queries that see them, and in no other of the same
     call: with each set to 0 the rest is the same to the bit."""
