@@ -259,7 +259,10 @@ int misa_score_topk_noalloc(const uint16_t* q, const float* w, const uint16_t* k
  * anything.  Reported and skipped: idx entries outside their query's prefix, tokens whose page
  * entry is not in [0, num_pages).  Reported and clamped: pos outside [-1, max_pages *
  * page_size).  q, out: dtype, [nseq, T, Hq, d]; lse (nullable) fp32 [nseq, T, Hq].  out may be
- * q itself; otherwise out and lse must not overlap one another, q or the caches.  Sums and softmax statistics are fp32; the weights p are rounded to dtype for their product with v.
+ * q itself; otherwise out and lse must not overlap one another, q or the caches.
+ * Sums and softmax statistics are fp32; the weights p are rounded to dtype for their product with
+ * v.  A row whose largest score is beyond what they hold (2^30 / log2 e = 7e8 in magnitude, in
+ * fp16 2^26 / log2 e = 4e7) is NaN.
  * A NaN or infinite key or value shows in the queries that see it, and in no other.
  * Made for few queries per sequence (decode, drafts): 128 / (Hq / Hkv) queries share one
  * reading of the cache.  ws: misa_paged_attention_workspace_size(...) bytes (0 where few or short items

@@ -134,6 +134,26 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// A weight's exponent is s scale2 - m in one rounding, m the largest score's product, rounded too.
+// So a row's largest weight is 2^x, x up to half a step of m: 2^-4 where m is 2^20 (log2 domain), 32
+// where it is 2^30, which bf16 and fp32 take.  fp16 ends at 2^16, so there m is rounded upward: the
+// weights get smaller at such scores, down to 2^-4 times where m is 2^26, but none overflows.
+// Beyond that the largest weight could come out as 0 or infinite, so a row's sum becomes NaN, and
+// with it its output.
+template <typename E>
+struct Weights {
+  static constexpr bool kFp16 = !IsBf16<E>::value;
+  // magnitude of a row's largest score: 2^26, 2^30
+  static constexpr float kLargest = kFp16 ? 67108864.f : 1073741824.f;
+  static __device__ __forceinline__ float reference(float top, float scale2) {
+    return kFp16 ? __fmul_ru(top, scale2) : top * scale2;
+  }
+  // the sum l of a row whose maximum has moved to m
+  static __device__ __forceinline__ float checked(float l, float m) {
+    return fabsf(m) > kLargest && m != -INFINITY ? NAN : l;   // -inf: no score yet
+  }
+};
+
 // Last token a query sees: pos[row] in [-1, cap); -1 sees nothing.  A value outside is
 // reported and clamped.
 __device__ __forceinline__ int last_token(const int32_t* __restrict__ pos, int64_t row, int cap,

@@ -281,7 +281,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
         t = fmaxf(t, fmaxf(s[r >> 1][x][(r & 1) * 2], s[r >> 1][x][(r & 1) * 2 + 1]));
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      mx[r] = fmaxf(m[r], t * a.scale2);
+      mx[r] = fmaxf(m[r], Weights<E>::reference(t, a.scale2));
       up |= mx[r] > m[r];
     }
     if (__any_sync(0xffffffffu, up)) {
@@ -289,7 +289,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
       for (int r = 0; r < 2 * MT; ++r) {
         const float f = mx[r] == m[r] ? 1.f : exp2_approx(m[r] - mx[r]);
         m[r] = mx[r];
-        l[r] *= f;
+        l[r] = Weights<E>::checked(l[r] * f, m[r]);
 #pragma unroll
         for (int x = 0; x < DN; ++x) {
           o[r >> 1][x][(r & 1) * 2] *= f;

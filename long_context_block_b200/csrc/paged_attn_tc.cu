@@ -314,11 +314,13 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
-          if (__any_sync(0xffffffffu, top > m + kSlack)) {   // the maximum moves, O with it
+          const float top =
+              Weights<E>::reference(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.scale2);
+          const float most = Weights<E>::kFp16 ? __fadd_rd(m, kSlack) : m + kSlack;
+          if (__any_sync(0xffffffffu, top > most)) {   // the maximum moves, O with it
             const float up = fmaxf(m, top), f = up == m ? 1.f : exp2_approx(m - up);
             m = up;
-            l *= f;
+            l = Weights<E>::checked(l * f, m);
             if (behind) {
               if (!(ok = warp_wait(odone, gi - 1))) break;
               behind = false;
