@@ -261,7 +261,8 @@ int misa_score_topk_noalloc(const uint16_t* q, const float* w, const uint16_t* k
  * page_size).  q, out: dtype, [nseq, T, Hq, d]; lse (nullable) fp32 [nseq, T, Hq].  out may be
  * q itself; otherwise out and lse must not overlap one another, q or the caches.
  * Sums and softmax statistics are fp32; the weights p are rounded to dtype for their product with
- * v.  A row whose largest score is beyond what they hold (2^30 / log2 e = 7e8 in magnitude, in
+ * v.  In fp16 those down to 2^-25 of their row's largest keep the type's precision, those below
+ * 2^-36 of it count as 0 there.  A row whose largest score is beyond what they hold (2^30 / log2 e = 7e8 in magnitude, in
  * fp16 2^26 / log2 e = 4e7) is NaN.
  * A NaN or infinite key or value shows in the queries that see it, and in no other.
  * Made for few queries per sequence (decode, drafts): 128 / (Hq / Hkv) queries share one

@@ -134,21 +134,29 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// A softmax weight is rounded to the 16-bit type for its product with V, as the matrix instruction
+// takes both factors in one type.  bf16 has fp32's exponents.  fp16 counts in steps of 2^-24 below
+// 2^-14, so there a row's reference m is taken below its largest score, which scales weights and sum
+// alike and leaves the quotient.  With the largest weight at 2^11 to 2^15, those down to 2^-25 of it
+// keep fp16's precision, and those below 2^-36 of it vanish (2^-14 and 2^-25 with the largest at 1).
+//
 // A weight's exponent is s scale2 - m in one rounding, m the largest score's product, rounded too.
-// So a row's largest weight is 2^x, x up to half a step of m: 2^-4 where m is 2^20 (log2 domain), 32
-// where it is 2^30, which bf16 and fp32 take.  fp16 ends at 2^16, so there m is rounded upward: the
-// weights get smaller at such scores, down to 2^-4 times where m is 2^26, but none overflows.
-// Beyond that the largest weight could come out as 0 or infinite, so a row's sum becomes NaN, and
-// with it its output.
+// So a row's largest weight is off by a factor 2^x, x up to half a step of m: 2^-4 where m is 2^20
+// (log2 domain), 32 where it is 2^30, which bf16 and fp32 take.  fp16 ends at 2^16, so there m is
+// rounded upward: the weights get smaller at such scores, down to 2^-8 times where m is 2^26, but
+// none overflows.  Beyond that the largest weight could come out as 0 or infinite, so a row's sum
+// becomes NaN, and with it its output.
 template <typename E>
 struct Weights {
   static constexpr bool kFp16 = !IsBf16<E>::value;
+  static constexpr float kTop = kFp16 ? 15.f : 0.f;   // log2 of the largest weight there can be
   // magnitude of a row's largest score: 2^26, 2^30
   static constexpr float kLargest = kFp16 ? 67108864.f : 1073741824.f;
-  static __device__ __forceinline__ float reference(float top, float scale2) {
-    return kFp16 ? __fmul_ru(top, scale2) : top * scale2;
+  // What a row's exponents are taken from (log2 domain): its largest score `top`, in fp16 less `up`.
+  static __device__ __forceinline__ float reference(float top, float scale2, float up) {
+    return kFp16 ? __fadd_ru(__fmul_ru(top, scale2), -up) : top * scale2;
   }
-  // the sum l of a row whose maximum has moved to m
+  // the sum l of a row whose reference has moved to m
   static __device__ __forceinline__ float checked(float l, float m) {
     return fabsf(m) > kLargest && m != -INFINITY ? NAN : l;   // -inf: no score yet
   }

@@ -270,7 +270,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
             if (!see) s[mt][x][y] = -INFINITY;
           }
     }
-    // the running maximum is kept in the log2 domain: m = max of the scores * scale2 (> 0)
+    // the running maximum is kept in the log2 domain: m = max of the scores * scale2 (> 0), in fp16
+    // less the exponent that the largest weight gets
     float mx[2 * MT];
     bool up = false;
 #pragma unroll
@@ -281,7 +282,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
         t = fmaxf(t, fmaxf(s[r >> 1][x][(r & 1) * 2], s[r >> 1][x][(r & 1) * 2 + 1]));
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      mx[r] = fmaxf(m[r], Weights<E>::reference(t, a.scale2));
+      mx[r] = fmaxf(m[r], Weights<E>::reference(t, a.scale2, Weights<E>::kTop));
       up |= mx[r] > m[r];
     }
     if (__any_sync(0xffffffffu, up)) {

@@ -1,11 +1,15 @@
 """The paged attention (GPU) at scores and weights far from the ordinary.  Cases and oracle as in
 test_gpu_paged.py."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_paged import M, Case, f64, form, i32   # noqa: F401 (M is a fixture)
+import oracle.paged_oracle as po
+
+from tests.test_gpu_paged import M, Case, f64, form   # noqa: F401 (M is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +88,50 @@ def test_scores_beyond_fp32_show(M, name):
     c.k[..., 0] = 2.0 ** 63
     out, lse = c.run(M)
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("gap", [11, 14, 17, 18])
+@pytest.mark.parametrize("name", list(EVERY_FORM))
+def test_an_attention_sink_over_a_long_tail(M, name, gap, dtype):
+    """A token with a zero value scores `gap` nats above all others, whose small weights make the
+    whole output.  The bound is Case.check's, and for fp16, whose steps below 2^-14 are 2^-24: a
+    weight is off by half a step, 2^-25, where the largest weight of its part is 2^11 at least, and
+    no part's largest score exceeds the row's.  So the sum over S tokens is off by S 2^-36 max|v|
+    more, over a sum of weights of 1 at least (both relative to the row's largest weight)."""
+    c = Case(**EVERY_FORM[name], dtype=dtype, poison=False, seed=gap)
+    assert form(M, c) == name.split("_")[0]
+    d = c.q.shape[-1]
+    c.q[..., 0] = 8
+    c.k.mul_(0.05)
+    c.k[..., 0] = 0
+    c.v = (100 + 10 * c.v.float()).to(c.v.dtype)
+    for n in range(len(c.lens)):
+        at = 0 if n % 2 == 0 else c.lens[n] // 3         # first, or in the middle
+        page, off = c.table[n, at // c.ps], at % c.ps
+        c.k[page, off] = 0
+        c.k[page, off, :, 0] = gap / (8 * c.scale)
+        c.v[page, off] = 0
+        if c.topk:
+            for t in range(c.T):
+                if at not in c.idx[n, t]:
+                    c.idx[n, t, c.topk // 2] = at
+    out, lse = c.run(M)
+    assert M.misa_check_device_status(out.device) == 0
+    q, k, v, got, lse = f64(c.q), f64(c.k), f64(c.v), f64(out), f64(lse)
+    u, e = torch.finfo(c.q.dtype).eps / 2, 2.0 ** -23
+    least = torch.finfo(c.q.dtype).tiny * u
+    for n in (0, 1, len(c.lens) - 1):
+        for t in {0, c.T - 1}:
+            seen = c.seen(n, t)
+            ref, rl, mean, mag = po.attention_row(q[n, t], k, v, c.table[n], c.ps, seen, c.scale)
+            S, dz = len(seen), (d + 8) * e * mag
+            w = u + 2 * dz + 2.0 ** -22 + 2 * (S + 16) * e
+            bound = u * 1.02 * np.abs(ref) + w[:, None] * mean + least
+            if dtype == "fp16":
+                bound += S * 2.0 ** -36 * np.abs(v).max()
+            err = np.abs(got[n, t] - ref)
+            assert np.all(err <= bound), (n, t, float((err / bound).max()))
+            assert np.all(np.abs(lse[n, t] - rl)
+                          <= dz + 2.0 ** -22 + (S + 16) * e + 4 * e * np.abs(rl)), (n, t)
+            assert 0 < ref.mean() < 60 and math.isfinite(rl.sum())
