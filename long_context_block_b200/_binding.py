@@ -202,15 +202,16 @@ _STATUS = _Status()
 
 
 def misa_check_device_status(device=None) -> int:
-    """Synchronise the current stream, read and clear the status words (the workspace's and the
-    paged-cache calls'); raise if one is set."""
-    dev = torch.device(device if device is not None else torch.cuda.current_device())
-    ws = _WS.get(256, dev)
-    st = int(_lib.misa_check_device_status(_ptr(ws), _stream()))
-    word = _STATUS.find(dev.index if dev.index is not None else torch.cuda.current_device())
-    paged = int(_lib.misa_check_device_status(_ptr(word), _stream())) if word is not None else 0
-    _check("misa_check_device_status", st or paged)
-    return st
+    """Synchronise the current stream, read and clear the status words (the workspace's, then the
+    paged-cache calls'); raise if one is set.  Where both are, the second stays for the next call."""
+    dev = torch.device(device if device is not None else "cuda")
+    if dev.index is None:      # the current device, whose buffers are kept under its number
+        dev = torch.device("cuda", torch.cuda.current_device())
+    for word in (_WS.get(256, dev), _STATUS.find(dev.index)):
+        if word is not None:
+            _check("misa_check_device_status",
+                   int(_lib.misa_check_device_status(_ptr(word), _stream())))
+    return 0
 
 
 def misa_pool_keys(k: torch.Tensor, B: int, out: torch.Tensor | None = None) -> torch.Tensor:
