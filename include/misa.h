@@ -22,7 +22,9 @@
  *     w      fp32  [nseq, T, H]       head weights w^I
  *     k      bf16  [nseq, L, d]       indexer keys k^I (one key stream per sequence)
  *     pos    int32 [nseq, T]          absolute position of each query; query (n, t)
- *                                     sees keys s = 0 .. pos[n,t] (prefix P = pos+1)
+ *                                     sees keys s = 0 .. pos[n,t] (prefix P = pos+1);
+ *                                     -1: a padded row, which sees nothing: its idx is all
+ *                                     -1, its heads are those of position 0
  *     k_pool fp32  [nseq, ceil(L/B), d]
  *     heads  int32 [nseq, T, h]
  *     E      fp32  [nseq, T, H]
@@ -37,7 +39,7 @@
  *   enqueue work; none of them synchronises, except misa_check_device_status.
  * Errors.  Every call returns a status (MISA_OK = 0).  Arguments are validated on
  *   the host before anything is enqueued; an invalid call enqueues nothing.
- *   Conditions only the GPU can see (a pos[] entry >= L, a candidate outside its
+ *   Conditions only the GPU can see (a pos[] entry outside [-1, L), a candidate outside its
  *   query's prefix, a bounded wait that expired) are recorded in the workspace
  *   status word; the affected values are clamped or skipped, never read out of
  *   bounds.  misa_check_device_status() reports and clears that word.
@@ -160,7 +162,8 @@ int dsa_score_topk(const uint16_t* q, const float* w, const uint16_t* k,
 /*
  * Token scores without selection: Eq. (9) over each query's prefix when heads is given
  * (h heads per query), Eq. (1) with all H heads when heads is NULL.  scores is fp32
- * [nseq, T, L]; entries s > pos are left untouched.  This is the scoring kernel of
+ * [nseq, T, L]; entries s > pos are left untouched (but for entry 0 of a padded
+ * row, which is not defined).  This is the scoring kernel of
  * misa_score_topk / dsa_score_topk on its own (same launch configuration), for callers
  * that select tokens themselves or inspect the scores.
  * Needs misa_workspace_size(MISA_OP_SCORE_ROWS, ...) (h = H when heads is NULL).

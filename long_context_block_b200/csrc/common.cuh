@@ -42,14 +42,21 @@ __device__ __forceinline__ void set_status(int* status, int code) {
   if (status) atomicCAS(status, 0, code);
 }
 
-// Prefix length of a query, clamped to [1, L]; out-of-range positions are reported.
+// Prefix length of a query, clamped to [1, L]; out-of-range positions are reported.  A padded row
+// (pos = -1) counts as one of position 0, so that routing and scoring need no case of their own; the
+// selection leaves it empty (row_len).
 __device__ __forceinline__ int prefix_len(const int32_t* pos, int64_t row, int64_t L, int* status) {
   int p = pos[row];
   if (p < 0 || (int64_t)p >= L) {
-    set_status(status, MISA_ERR_BAD_DEVICE_INPUT);
+    if (p != -1) set_status(status, MISA_ERR_BAD_DEVICE_INPUT);
     p = p < 0 ? 0 : (int)(L - 1);
   }
   return p + 1;
+}
+
+// Tokens that a query's selection is made from: its prefix, nothing for a padded row.
+__device__ __forceinline__ int row_len(const int32_t* pos, int64_t row, int64_t L, int* status) {
+  return pos[row] == -1 ? 0 : prefix_len(pos, row, L, status);
 }
 
 }  // namespace misa

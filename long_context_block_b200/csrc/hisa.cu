@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(256) hisa_expand_kernel(
     int32_t* __restrict__ count, int64_t row0) {
   pdl_prologue();
   const int64_t row = row0 + blockIdx.x;
-  const int P = prefix_len(pos, row, L, nullptr);
+  const int P = row_len(pos, row, L, nullptr);
   const int nb = min(max(bcount[row], 0), m);
   const int32_t* blocks = sb + row * m;
   int32_t* out = tok + row * span;
@@ -85,7 +85,7 @@ cudaError_t launch_hisa(const uint16_t* q, const float* w, const uint16_t* k, co
   cudaError_t e = launch_block_scores(q, w, k, k_pool, pos, nseq, T, H, L, B, G, last_block,
                                       status, st);
   if (e != cudaSuccess) return e;
-  // row r holds M_t = last_block[r] + 1 block scores
+  // row r holds M_t = last_block[r] + 1 block scores (a padded row none)
   e = launch_topk(G, Mpool, last_block, Mpool, nullptr, nullptr, rows, m, blk, nullptr, status,
                   st);
   if (e != cudaSuccess) return e;

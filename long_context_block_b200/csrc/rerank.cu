@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kBitmapThreads) bitmap_candidates_kernel(
   __shared__ uint32_t warp_sums[kBitmapThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = row0 + blockIdx.x;
-  const int P = prefix_len(pos, row, L, tid == 0 ? status : nullptr);
+  const int P = row_len(pos, row, L, tid == 0 ? status : nullptr);
   const int nwords = (P + 31) >> 5;
   for (int i = tid; i < nwords; i += kBitmapThreads) bm[i] = 0u;
   __syncthreads();
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kBitmapThreads) bitmap_candidates_split_kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slices = (int)gridDim.x, slice = (int)blockIdx.x;
   const int64_t row = row0 + blockIdx.y;
-  const int P = prefix_len(pos, row, L, tid == 0 && slice == 0 ? status : nullptr);
+  const int P = row_len(pos, row, L, tid == 0 && slice == 0 ? status : nullptr);
   const int nwords = (P + 31) >> 5;
   const int wps = (nwords + slices - 1) / slices;
   const int sw0 = min(slice * wps, nwords), sw1 = min(sw0 + wps, nwords);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) sort_candidates_kernel(
   extern __shared__ uint64_t buf[];   // [sortn]
   const int tid = threadIdx.x;
   const int64_t row = row0 + blockIdx.x;
-  const int P = prefix_len(pos, row, L, tid == 0 ? status : nullptr);
+  const int P = row_len(pos, row, L, tid == 0 ? status : nullptr);
   __shared__ int s_count;
   if (tid == 0) s_count = 0;
   __syncthreads();

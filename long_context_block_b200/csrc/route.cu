@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kRouteThreads) block_score_kernel(
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = prefix_len(pos, row, L, chunk == 0 && tid == 0 ? status : nullptr);
   const int M = (P + B - 1) / B;
-  if (chunk == 0 && tid == 0) last_block[row] = M - 1;
+  if (chunk == 0 && tid == 0) last_block[row] = pos[row] == -1 ? -1 : M - 1;
   const int b0 = chunk * kCh;
   if (b0 >= M) return;
   const int nb = min(b0 + kCh, M) - b0;

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) topk_kernel(
   __shared__ uint32_t warp_sums[32];
   __shared__ uint32_t s_digit, s_above, s_cnt;
   const int64_t row = row0 + blockIdx.x;
-  const int n = gather_len ? gather_len[row] : prefix_len(pos, row, L, nullptr);
+  const int n = gather_len ? gather_len[row] : row_len(pos, row, L, nullptr);
   select_row_global(scores + row * stride, index_map ? index_map + row * stride : nullptr, n, topk,
                     sortn, sel, hist, warp_sums, s_digit, s_above, s_cnt);
   sort_buf_desc(sel, sortn);
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) topk_cluster_kernel(
   const int crank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t row = blockIdx.x / G;
-  const int n = gather_len ? gather_len[row] : prefix_len(pos, row, L, nullptr);
+  const int n = gather_len ? gather_len[row] : row_len(pos, row, L, nullptr);
   const float* x = scores + row * stride;
   const int32_t* imap = index_map ? index_map + row * stride : nullptr;
   int slice = (n + G - 1) / G;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kSelThreads) topk_scatter_kernel(
   __shared__ uint32_t s_cut, s_total, s_big;
   const int t = threadIdx.x;
   const int64_t row = blockIdx.y;
-  const int n = prefix_len(pos, row, L, nullptr);
+  const int n = row_len(pos, row, L, nullptr);
   const int start = blockIdx.x * kScatterChunk;
   if (start >= n) return;
   if (t < kMaxGroups) lcount[t] = 0;
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) topk_group_kernel(
   const int t = threadIdx.x;
   const int64_t row = blockIdx.y;
   const uint32_t g = blockIdx.x;
-  const int n = prefix_len(pos, row, L, nullptr);
+  const int n = row_len(pos, row, L, nullptr);
   const uint32_t target = (uint32_t)min(n, topk);
   if (t == 0) { s_lo = 0xffffffffu; s_hi = 0; s_start = 0xffffffffu; s_cnt = 0; }
   HistView<kSelThreads> hv;
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) topk_group_kernel(
       if (vals) vals[row * topk + i] = __int_as_float(0xff800000);
     }
   const uint32_t cnt = min(s_cnt, (uint32_t)kGroupBuf);
-  if (cnt == 0) return;
+  if (cnt == 0 || target == 0) return;   // (a padded row has a score in its histogram)
   const uint32_t blo = s_lo, bhi = s_hi, start = s_start;
   const uint64_t* src = cand + row * (int64_t)hist_groups(topk) * kGroupBuf + g * kGroupBuf;
   for (uint32_t i = t; i < cnt; i += kSelThreads) gathered[i] = src[i];
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kSelThreads) topk_build_hist_kernel(
   __shared__ uint32_t sh[kScoreHistBins];
   const int t = threadIdx.x;
   const int64_t row = blockIdx.y;
-  const int n = prefix_len(pos, row, L, nullptr);
+  const int n = row_len(pos, row, L, nullptr);
   const int start = blockIdx.x * kScatterChunk;
   if (start >= n) return;
   for (int b = t; b < kScoreHistBins; b += kSelThreads) sh[b] = 0;
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads) topk_hist_overflow_kernel(
   __shared__ uint32_t warp_sums[32];
   __shared__ uint32_t s_cut, s_total, s_big, s_digit, s_above, s_cnt;
   const int64_t row = blockIdx.x;
-  const int n = prefix_len(pos, row, L, nullptr);
+  const int n = row_len(pos, row, L, nullptr);
   HistView<kThreads> hv;
   hist_cutoff<kThreads>(hist + row * kScoreHistBins, (uint32_t)min(n, topk), hv, warp_sums, s_cut,
                         s_total, s_big);
@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(NT, MINB) topk_row_kernel(
   __shared__ __align__(8) uint64_t lbar;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t row = row0 + blockIdx.x;
-  const int n = gather_len ? gather_len[row] : prefix_len(pos, row, L, nullptr);
+  const int n = gather_len ? gather_len[row] : row_len(pos, row, L, nullptr);
   const uint32_t target = (uint32_t)min(n, topk);
   const float* x = scores + row * stride;
   const int32_t* imap = index_map ? index_map + row * stride : nullptr;
