@@ -57,13 +57,34 @@ struct Shape {
   static_assert(kWarps * RB * OSTR * 4 <= RING, "the join buffer lies in the ring");
 };
 
+// What the dropped values add, by the whole CTA: a warp takes a quarter of the columns of all rows,
+// and a row's go to its part of the largest weights.  Not inlined: as add_non_finite.
+template <typename E, int D, int RB, int OSTR>
+__device__ __noinline__ void add_to_parts(const AttnArgs& a, Part p, const Dropped& dropped,
+                                          float* s_o, const float2 (*s_ml)[RB]) {
+  constexpr int C = D / kWarps;
+  static_assert(C <= 32 && RB <= 32, "a lane per column, a lane per row");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const NonFinite f = non_finite<E, D>(a, p, dropped, lane, lane < p.rows, warp * C, C);
+  for (int r = 0; r < p.rows; ++r) {
+    NonFinite x = {};
+    x.plus[0] = __shfl_sync(0xffffffffu, f.plus[0], r);
+    x.minus[0] = __shfl_sync(0xffffffffu, f.minus[0], r);
+    if (lane >= C || x.at(lane) == 0.f) continue;
+    int w = 0;
+    for (int y = 1; y < kWarps; ++y)
+      if (s_ml[y][r].x > s_ml[w][r].x) w = y;
+    s_o[(w * RB + r) * OSTR + warp * C + lane] += x.at(lane);
+  }
+}
+
 // Tokens tok0 .. tok1 - 1 of entry `en` (of the prefix, or slots of its idx row) for key-value
 // head hk, by the whole CTA.  Leaves each warp's part in shared memory: weighted values at
 // smem (rows of OSTR floats, warp-major), maximum and sum in s_ml.
 template <typename E, int D, int MT, bool SEL>
 __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, SEL>& en, int hk,
                                        int tok0, int tok1, unsigned char* smem,
-                                       float2 (*s_ml)[16 * MT]) {
+                                       float2 (*s_ml)[16 * MT], Dropped& dropped) {   // cleared
   using S = Shape<D, MT>;
   constexpr int RB = S::RB, KT = S::KT, UNIT = S::UNIT, ROWB = S::ROWB, CH = S::CH,
                 TILE = S::TILE;
@@ -253,6 +274,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
         uint4 x = *at;
         if (drop_non_finite<E>(x)) {
           *at = x;
+          dropped.add(s0 + r - tok0, tok1 - tok0);
           drop = true;
         }
       }
@@ -352,15 +374,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
   if (SEL) {
     __syncthreads();
   } else if (__syncthreads_or(drop)) {
-    const Part at{en.n, en.row0, en.rows, hk, tok0, tok1};
-    for (int r = warp; r < en.rows; r += kWarps) {
-      int w = 0;   // to the part of the largest weights
-      for (int x = 1; x < kWarps; ++x)
-        if (s_ml[x][r].x > s_ml[w][r].x) w = x;
-      if (lane < D / 4)
-        add_non_finite<E, D>(a, at, r, lane * 4, 4, s_o + (w * RB + r) * S::OSTR + lane * 4);
-    }
+    add_to_parts<E, D, RB, S::OSTR>(a, {en.n, en.row0, en.rows, hk, tok0, tok1}, dropped, s_o, s_ml);
     __syncthreads();
+    dropped.clear(tid);
   }
 }
 
@@ -390,6 +406,8 @@ paged_attn_cluster_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ float2 s_ml[kWarps][S::RB];
   __shared__ float2 s_part[S::RB];
+  __shared__ Dropped s_dropped;
+  if (!SEL) s_dropped.clear(threadIdx.x);
   pdl_prologue();
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -399,7 +417,7 @@ paged_attn_cluster_kernel(const __grid_constant__ AttnArgs a) {
   const int64_t units = (ntok + S::UNIT - 1) / S::UNIT;
   const int tok0 = (int)(rank * units / size) * S::UNIT;
   const int tok1 = min(ntok, (int)((rank + 1) * units / size) * S::UNIT);
-  attend<E, D, MT, SEL>(a, en, hk, tok0, tok1, smem, s_ml);
+  attend<E, D, MT, SEL>(a, en, hk, tok0, tok1, smem, s_ml, s_dropped);
   float* s_o = reinterpret_cast<float*>(smem);
   const int work = en.rows * (D / 4);
   if (size > 1) {   // this CTA's sum takes the place of its first warp's part
@@ -449,7 +467,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ float2 s_ml[kWarps][RB];
   __shared__ typename R::Shared s_range;
+  __shared__ Dropped s_dropped;
   const int cta = blockIdx.x;
+  if (!SEL) s_dropped.clear(threadIdx.x);
   pdl_prologue();
   R range;
   typename R::Segment sg;
@@ -459,7 +479,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       const Entry<RB, SEL> en(a, sg.e);
       const int hk = sg.hk, tok0 = sg.uo * UNIT;
       const int tok1 = min(sg.ntok, (sg.uo + sg.take) * UNIT);
-      attend<E, D, MT, SEL>(a, en, hk, tok0, tok1, smem, s_ml);
+      attend<E, D, MT, SEL>(a, en, hk, tok0, tok1, smem, s_ml, s_dropped);
       const bool whole = sg.take == sg.units;
       const int slot = 2 * cta + (sg.uo == 0 ? 1 : 0);
       for (int i = threadIdx.x; i < en.rows * (D / 4); i += kThreads) {

@@ -140,23 +140,107 @@ __device__ __forceinline__ void add_part(float4& acc, float& ll, float mm, float
 
 // A draft's later tokens lie in the same tiles as those that its earlier queries see, with weight 0
 // for them, but 0 times a NaN or infinite value is NaN.  So such values of tokens that not every
-// row of the block sees are set to 0 in shared memory, and this adds them, from the cache, to the
-// elements c .. c + n - 1 (at `to`) of a row that sees them: a weight is positive, and any positive
-// weight gives the same sum.  Not inlined, as its code slows down short calls: 0.5 us of 10 us.
-template <typename E, int D, typename O>
-__device__ __noinline__ void add_non_finite(const AttnArgs& a, Part p, int r, int c, int n, O* to) {
-  const int cap = a.max_pages * a.page_size;
-  const int last = min(p.tok1 - 1, last_token(a.pos, (int64_t)p.n * a.T + (p.row0 + r) / a.G, cap,
-                                              nullptr));
-  if (last < p.tok0) return;
-  for (int s = seen_by_all(a, p, 1, 0) + 1; s <= last; ++s) {
-    const int row = cache_row(a.table + (int64_t)p.n * a.max_pages, s, a.page_size, a.by_page,
-                              a.num_pages, nullptr);
-    if (row < 0) continue;
-    const E* v = static_cast<const E*>(a.v) + ((int64_t)row * a.Hkv + p.hk) * D + c;
-    for (int i = 0; i < n; ++i) {
-      const float x = to_f32(v[i]);
-      if (!isfinite(x)) to[i] = from_f32<O>(to_f32(to[i]) + x);
+// row of the block sees are set to 0 in shared memory, which tokens they were is kept (Dropped), and
+// afterwards they are looked up in the cache and added to the rows that see them: a weight is
+// positive, and any positive weight gives the same sum.
+//
+// Dropped holds a bit for every bucket of a segment's tokens, so that only these are read again: one
+// value between two queries 32768 tokens apart costs 32 tokens, not 32768 (which took longer than
+// the tensor-core form's waits in a test with short ones).
+struct Dropped {
+  static constexpr int kBuckets = 1024;
+  uint32_t bits[kBuckets / 32];
+  static __device__ __forceinline__ int shift(int tokens) {   // 2^shift tokens to a bucket
+    return max(0, 22 - __clz(tokens - 1));
+  }
+  __device__ __forceinline__ void clear(int thread) {
+    if (thread < kBuckets / 32) bits[thread] = 0u;
+  }
+  __device__ __forceinline__ void add(int at, int tokens) {   // token `at` of a segment's
+    const int b = at >> shift(tokens);
+    atomicOr(&bits[b >> 5], 1u << (b & 31));
+  }
+};
+
+// What the dropped values add to a row, in 64 neighbouring columns: +inf (bit x of plus[i]: column
+// 32 i + x), -inf, or NaN where both are.
+struct NonFinite {
+  uint32_t plus[2], minus[2];
+  __device__ __forceinline__ float at(int c) const {
+    const bool p = (plus[c >> 5] >> (c & 31)) & 1u, m = (minus[c >> 5] >> (c & 31)) & 1u;
+    return p && m ? NAN : p ? INFINITY : m ? -INFINITY : 0.f;
+  }
+};
+
+// By a converged warp, a lane per row r (`mine`: the row exists and has a sum): columns c0 ..
+// c0 + nc - 1, at most 64.
+template <typename E, int D>
+__device__ __forceinline__ NonFinite non_finite(const AttnArgs& a, Part p, const Dropped& dropped,
+                                             int r, bool mine, int c0, int nc) {
+  constexpr int U = 4;   // tokens whose values are read at once
+  const int lane = threadIdx.x & 31, cap = a.max_pages * a.page_size, shift = Dropped::shift(p.tok1 - p.tok0);
+  const int last =
+      mine ? last_token(a.pos, (int64_t)p.n * a.T + (p.row0 + r) / a.G, cap, nullptr) : -1;
+  const int seen = __reduce_min_sync(0xffffffffu, seen_by_all(a, p, 32, lane));
+  NonFinite f = {{0u, 0u}, {0u, 0u}};
+  uint32_t word = 0;
+  for (int w = 0; w < Dropped::kBuckets / 32 || word != 0;) {
+    if (word == 0) {
+      word = dropped.bits[w++];
+      continue;
+    }
+    const int b = 32 * (w - 1) + __ffs(word) - 1;
+    word &= word - 1u;
+    const int end = p.tok0 + min((b + 1) << shift, p.tok1 - p.tok0);
+    for (int s0 = max(p.tok0 + (b << shift), seen + 1); s0 < end; s0 += 32) {
+      const int row = s0 + lane < end
+                          ? cache_row(a.table + (int64_t)p.n * a.max_pages, s0 + lane, a.page_size,
+                                      a.by_page, a.num_pages, nullptr)
+                          : -1;
+      const int n = min(32, end - s0);
+      for (int j = 0; j < n; j += U) {
+        float x[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int at = __shfl_sync(0xffffffffu, row, (j + u) & 31);
+          const E* v = static_cast<const E*>(a.v) + ((int64_t)max(at, 0) * a.Hkv + p.hk) * D + c0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            x[u][i] = j + u < n && at >= 0 && lane + 32 * i < nc ? to_f32(v[lane + 32 * i]) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t plus =
+                __ballot_sync(0xffffffffu, isnan(x[u][i]) || x[u][i] == INFINITY);
+            const uint32_t minus =
+                __ballot_sync(0xffffffffu, isnan(x[u][i]) || x[u][i] == -INFINITY);
+            if (s0 + j + u <= last) {
+              f.plus[i] |= plus;
+              f.minus[i] |= minus;
+            }
+          }
+      }
+    }
+  }
+  return f;
+}
+
+// The same, added to the half of row r that begins at column c0 and lies at `to`, of type E (narrow)
+// or fp32.  Not inlined, as its code slows down short calls: 0.5 us of 10 us.
+template <typename E, int D>
+__device__ __noinline__ void add_non_finite(const AttnArgs& a, Part p, const Dropped& dropped, int r,
+                                            bool mine, int c0, void* to, bool narrow) {
+  const NonFinite f = non_finite<E, D>(a, p, dropped, r, mine, c0, D / 2);
+  for (int c = 0; c < D / 2; ++c) {
+    const float x = f.at(c);
+    if (x == 0.f) continue;
+    if (narrow) {
+      E* y = static_cast<E*>(to) + c;
+      *y = from_f32<E>(to_f32(*y) + x);
+    } else {
+      static_cast<float*>(to)[c] += x;
     }
   }
 }

@@ -184,8 +184,9 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ float2 s_ml[2][2][kRows];   // [segment parity][group][row]
-  __shared__ int s_non_finite;           // a value that not every row sees was NaN or infinite and
-                                         // left out, in this segment or one before
+  // values of this segment that not every row sees were NaN or infinite and left out; their tokens
+  __shared__ int s_non_finite;
+  __shared__ Dropped s_dropped;
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
@@ -196,6 +197,7 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   volatile int* abort_flag = &s_abort;
 
+  if (!SEL) s_dropped.clear(tid);
   if (tid == 0) {
     s_abort = s_non_finite = 0;
     for (int i = 0; i < C::kKStages; ++i) {
@@ -420,14 +422,12 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
               store32(out + x, reinterpret_cast<const uint32_t*>(o + x));
           }
         }
-        if (!SEL && mine && n > 0 && *static_cast<volatile int*>(&s_non_finite)) {
+        if (!SEL && n > 0 && *static_cast<volatile int*>(&s_non_finite)) {
           const int c = group * (D / 2);
-          const Part at{en.n, en.row0, en.rows, sg.hk, tok0, tok1};
-          if (whole)
-            add_non_finite<E, D>(a, at, row, c, D / 2, static_cast<E*>(a.out) + head * D + c);
-          else
-            add_non_finite<E, D>(a, at, row, c, D / 2,
-                                 a.part_o + ((int64_t)slot * kRows + row) * D + c);
+          void* to = whole ? static_cast<void*>(static_cast<E*>(a.out) + head * D + c)
+                           : a.part_o + ((int64_t)slot * kRows + row) * D + c;
+          add_non_finite<E, D>(a, {en.n, en.row0, en.rows, sg.hk, tok0, tok1}, s_dropped, row,
+                               mine && l != 0.f, c, to, whole);
         }
         if (mine && group == 0) {
           if (!whole)
@@ -608,6 +608,12 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
       if (!(ok = seg == 0 ? warp_wait(qfirst, 0) : warp_wait(qfull, seg - 1))) break;
       if (!(ok = scores(g, n == 1)) || (n > 1 && !(ok = scores(g + 1, n == 2)))) break;
       if (seg > 0 && !(ok = warp_wait(ofree, seg - 1))) break;
+      if (!SEL && s_non_finite) {   // the segment before is through with them
+        __syncwarp();
+        s_dropped.clear(lane);
+        s_non_finite = 0;
+        __syncwarp();
+      }
       if (!SEL) seen = __reduce_min_sync(0xffffffffu, seen);
       for (int i = 0; i < n; ++i) {
         const int gi = g + i, st = gi % C::kVStages, buf = gi & 1;
@@ -627,6 +633,7 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
             uint4 y = *at;
             if (drop_non_finite<E>(y)) {
               *at = y;
+              s_dropped.add(s0 + r - tok0, tok1 - tok0);
               drop = true;
             }
           }

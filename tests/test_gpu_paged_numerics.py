@@ -135,3 +135,115 @@ def test_an_attention_sink_over_a_long_tail(M, name, gap, dtype):
             assert np.all(np.abs(lse[n, t] - rl)
                           <= dz + 2.0 ** -22 + (S + 16) * e + 4 * e * np.abs(rl)), (n, t)
             assert 0 < ref.mean() < 60 and math.isfinite(rl.sum())
+
+
+# ------------------------------------------------------- values that only some queries see
+
+DRAFTS = {
+    "cluster_draft4": dict(lens=[900, 40, 2, 130], T=4),
+    "cluster_draft16_d64": dict(lens=[700, 64], T=16, Hq=4, Hkv=2, d=64, dtype="fp16", ps=48),
+    "ranges_draft4_d64": dict(lens=[3000, 2, 30000], T=4, Hq=8, Hkv=2, d=64, ps=128),
+    "ranges_draft8": dict(lens=[9000, 20000], T=8, Hq=8, Hkv=2, ps=64),
+    "tc_one_tile": dict(lens=[90, 33, 77], T=9, Hq=8, Hkv=2, d=64, ps=8, dtype="fp16"),
+    "tc_whole_draft": dict(lens=[7 * i for i in range(60)], T=16, Hq=8, Hkv=1, d=64, ps=32),
+    "tc_ranges_draft": dict(lens=[(i * 61) % 700 for i in range(90)], T=16, Hq=8, Hkv=2, ps=100),
+    "tc_long_one": dict(lens=[70000], T=5, Hq=8, Hkv=1, ps=64),
+    "tc_two_blocks": dict(lens=[2300 - 40 * i for i in range(20)], T=16, Hq=12, Hkv=1, d=64, ps=32),
+}
+
+
+def classes(t):
+    """Finite values as they are, one number for each kind of the others."""
+    return torch.nan_to_num(t.float().cpu(), 7e7, 8e7, 9e7)
+
+
+@pytest.mark.parametrize("name", list(DRAFTS))
+def test_values_between_positions_far_apart(M, name):
+    """Queries anywhere in their sequence, and NaN and infinite values anywhere between them: they
+    show in the queries that see them and in no other; the rest is the same to the bit."""
+    c = Case(**DRAFTS[name], poison=False, seed=2)
+    assert form(M, c) == name.split("_")[0]
+    rng = np.random.default_rng(7)
+    for n, x in enumerate(c.lens):
+        if x > 1:
+            c.pos[n] = rng.integers(0, x, c.T)
+            c.pos[n, -1], c.pos[n, 0] = x - 1, x // 9
+    H, d = c.k.shape[2:]
+    special = [float("nan"), float("inf"), -float("inf")]
+    marks = {}
+    for n, x in enumerate(c.lens):
+        for _ in range(40 if len(c.lens) < 5 else 4):
+            s = int(rng.integers(x // 9 + 1, x)) if x // 9 + 1 < x else x - 1
+            if s >= 0:
+                row = (c.table[n, s // c.ps], s % c.ps, int(rng.integers(H)), int(rng.integers(d)))
+                marks[row] = (n, s, special[int(rng.integers(3))])
+    for row in marks:
+        c.v[row] = 0
+    ref, lse = c.run(M)
+    want, G = ref.float().cpu(), c.q.shape[2] // H
+    for row, (n, s, x) in marks.items():
+        c.v[row] = x
+        for t in range(c.T):
+            if c.pos[n, t] >= s:
+                want[n, t, row[2] * G:(row[2] + 1) * G, row[3]] += x
+    out, lse2 = c.run(M)
+    assert M.misa_check_device_status(out.device) == 0
+    assert torch.equal(lse, lse2) and torch.equal(classes(out), classes(want))
+    assert not torch.isfinite(want).all() and torch.isfinite(want).float().mean() > 0.5
+
+
+@pytest.mark.parametrize("name", list(DRAFTS))
+def test_scores_of_minus_infinity_below_infinite_values(M, name):
+    """A query whose scores are all -inf sees nothing, also where its tokens' values are infinite and
+    shorter queries of its block do not see them.  The other columns and queries have what each
+    query has in a call of its own, and infinite values of a finite score show."""
+    c = Case(**DRAFTS[name], poison=False, seed=4)
+    c.q.abs_().add_(0.5)
+    for n, x in enumerate(c.lens):
+        if x <= 20:
+            continue
+        c.pos[n, 0], c.pos[n, 1] = 1, 9
+        for s in range(10):
+            c.k[c.table[n, s // c.ps], s % c.ps, :, 7] = -float("inf")
+        c.v[c.table[n, 5 // c.ps], 5 % c.ps, :, 9] = float("inf")
+        at = (c.table[n, (x - 2) // c.ps], (x - 2) % c.ps)
+        c.v[at][:, 3] = float("inf")
+        c.v[at][:, 5] = -float("inf")
+    out, lse = c.run(M)
+    a = [x.cuda() for x in (c.q, c.k, c.v)]
+    table, pos = torch.from_numpy(c.table).cuda(), torch.from_numpy(c.pos).cuda()
+    alone = torch.stack([M.misa_paged_attention(a[0][:, t].unsqueeze(1).contiguous(), a[1], a[2],
+                                                table, pos[:, t:t + 1].contiguous(),
+                                                scale=c.scale)[:, 0] for t in range(c.T)], 1)
+    assert M.misa_check_device_status(out.device) == 0
+    for n, x in enumerate(c.lens):
+        if x > 20:
+            assert bool((out[n, :2] == 0).all()) and torch.isneginf(lse[n, :2]).all()
+            assert bool((alone[n, :2] == 0).all())
+            assert torch.isposinf(out[n, -2:, :, 3]).all() and torch.isneginf(out[n, -2:, :, 5]).all()
+    out[..., 9] = alone[..., 9] = 0              # an infinite value of weight 0: not defined
+    for f in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(f(out), f(alone))
+
+
+def test_one_infinite_value_does_not_hold_up_a_long_call(M):
+    """Drafts whose queries lie 32767 tokens apart, one infinite value between them: only its
+    neighbours are read again, so that no bounded wait of a millisecond runs out."""
+    n, L, T, Hq, d, ps = 320, 32768, 8, 8, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    k, v, q = r(L // ps, ps, 1, d), r(L // ps, ps, 1, d), r(n, T, Hq, d)
+    table = torch.arange(L // ps, dtype=torch.int32, device="cuda").repeat(n, 1)
+    pos = torch.full((n, T), L - 1, dtype=torch.int32, device="cuda")
+    pos[:, 0] = 0
+    v[300, 5, 0, 11] = 0
+    ref = M.misa_paged_attention(q, k, v, table, pos)
+    same = M.misa_testing_paged_attention_wait_expiry(q, k, v, table, pos, wait_cycles=2_000_000,
+                                                      skip_tile=-1)
+    assert M.misa_check_device_status("cuda") == 0 and torch.equal(same, ref)
+    v[300, 5, 0, 11] = float("inf")
+    out = M.misa_testing_paged_attention_wait_expiry(q, k, v, table, pos, wait_cycles=2_000_000,
+                                                     skip_tile=-1)
+    assert M.misa_check_device_status("cuda") == 0
+    ref[:, 1:, :, 11] = float("inf")
+    assert torch.equal(out, ref)
