@@ -262,7 +262,7 @@ int misa_score_topk_noalloc(const uint16_t* q, const float* w, const uint16_t* k
  * anything.  Reported and skipped: idx entries outside their query's prefix, tokens whose page
  * entry is not in [0, num_pages).  Reported and clamped: pos outside [-1, max_pages *
  * page_size).  q, out: dtype, [nseq, T, Hq, d]; lse (nullable) fp32 [nseq, T, Hq].  out may be
- * q itself; otherwise out and lse must not overlap one another, q or the caches.
+ * q itself; otherwise what is written (out, lse, ws, device_status) must not overlap anything else.
  * Sums and softmax statistics are fp32; the weights p are rounded to dtype for their product with
  * v.  In fp16 those down to 2^-25 of their row's largest keep the type's precision, those below
  * 2^-36 of it count as 0 there.  A row whose largest score is beyond what they hold (2^30 / log2 e = 7e8 in magnitude, in
@@ -290,7 +290,8 @@ int misa_paged_attention(const void* q, const void* k_cache, const void* v_cache
  * (with two for one, which of them each 16 bytes come from is undefined), and a page that others
  * hold too is theirs as well: misa_pages_resize copies it first.  Reported and skipped: pos
  * outside [-1, max_pages * page_size), page entries outside [0, num_pages).  No workspace.
- * k_cache and v_cache must not overlap, and no row written may be one of k_new or v_new.
+ * What is written (the caches, device_status) must not overlap one another, pos or page_table, and
+ * no row written may be one of k_new or v_new.
  */
 int misa_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
                       const int32_t* page_table, int dtype, int nseq, int T, int Hkv, int d,
@@ -299,11 +300,11 @@ int misa_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
 
 /*
  * Upkeep of the pages.  Each call reads page_table and refs and writes out_table and out_refs,
- * which may be the same buffers (in place) but must not overlap them otherwise.  `pools` (a host
- * array of npools device pointers; NULL with npools 0) lists every pool that the table pages,
- * e.g. the k_cache and v_cache of all layers: pool i is [num_pages, page_bytes[i]], page_bytes[i]
- * a multiple of 16.  Pools must not overlap one another.  ws: misa_pages_workspace_size(op,
- * ...) bytes (0, and ws may be NULL, where none is needed; 0 on invalid arguments too).
+ * which may be the same buffers (in place); otherwise nothing that a call writes may overlap another
+ * of its buffers.  `pools` (a host array of npools device pointers; NULL with npools 0) lists every
+ * pool that the table pages, e.g. the k_cache and v_cache of all layers: pool i is [num_pages,
+ * page_bytes[i]], page_bytes[i] a multiple of 16.  ws: misa_pages_workspace_size(op, ...) bytes (0,
+ * and ws may be NULL, where none is needed; 0 on invalid arguments too).
  */
 size_t misa_pages_workspace_size(int op, int nseq, int max_pages, int num_pages);
 

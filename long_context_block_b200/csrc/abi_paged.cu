@@ -2,8 +2,10 @@
 // Declarations and contracts: include/misa.h.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "internal.h"
 #include "misa.h"
@@ -55,28 +57,59 @@ int check_scratch(void* ws, size_t ws_bytes, size_t need) {
   return check_dev(ws, need, 256);
 }
 
+struct Buffer {
+  const void* p;   // null: none
+  size_t bytes;
+};
+
+bool overlap(const Buffer& x, const Buffer& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return a != 0 && b != 0 && a < b + y.bytes && b < a + x.bytes;
+}
+
 // What is written must not overlap what another buffer holds.
-int check_apart(const void* x, size_t xb, const void* y, size_t yb) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-  return a < b + yb && b < a + xb ? MISA_ERR_INVALID_ARG : MISA_OK;
+int check_apart(std::initializer_list<Buffer> written, std::initializer_list<Buffer> read) {
+  for (const Buffer* x = written.begin(); x != written.end(); ++x) {
+    for (const Buffer* y = x + 1; y != written.end(); ++y)
+      if (overlap(*x, *y)) return MISA_ERR_INVALID_ARG;
+    for (const Buffer& y : read)
+      if (overlap(*x, y)) return MISA_ERR_INVALID_ARG;
+  }
+  return MISA_OK;
 }
 
-// out may be the input itself, but must not overlap it otherwise.
-int check_out(const void* in, const void* out, size_t bytes) {
-  return in == out ? MISA_OK : check_apart(in, bytes, out, bytes);
+// An input that the output may take the place of: none where it does.
+Buffer unless(const void* out, const Buffer& in) {
+  return {out == in.p ? nullptr : in.p, in.bytes};
 }
 
-int check_upkeep(int op, const int32_t* table, const int32_t* refs, int nseq, int max_pages,
-                 int num_pages, const int32_t* out_table, const int32_t* out_refs, void* ws,
-                 size_t ws_bytes) {
-  const size_t tb = (size_t)nseq * max_pages * 4, rb = (size_t)num_pages * 4;
-  MISA_TRY(check_dev(table, tb, 4));
-  MISA_TRY(check_dev(refs, rb, 4));
-  MISA_TRY(check_dev(out_table, tb, 4));
-  MISA_TRY(check_dev(out_refs, rb, 4));
-  MISA_TRY(check_out(table, out_table, tb));
-  MISA_TRY(check_out(refs, out_refs, rb));
-  return check_scratch(ws, ws_bytes, misa_pages_workspace_size(op, nseq, max_pages, num_pages));
+// The buffers of an upkeep call; x, y: its own inputs, nseq ints each.
+struct Upkeep {
+  const int32_t *table, *refs, *x, *y;
+  const int32_t *out_table, *out_refs, *n_live, *status;
+  const void* ws;
+};
+
+int check_upkeep(int op, const Upkeep& u, int nseq, int max_pages, int num_pages, size_t ws_bytes,
+                 const PagePools* pools) {
+  const size_t tb = (size_t)nseq * max_pages * 4, rb = (size_t)num_pages * 4, nb = (size_t)nseq * 4;
+  const size_t need = misa_pages_workspace_size(op, nseq, max_pages, num_pages);
+  MISA_TRY(check_dev(u.table, tb, 4));
+  MISA_TRY(check_dev(u.refs, rb, 4));
+  MISA_TRY(check_dev(u.out_table, tb, 4));
+  MISA_TRY(check_dev(u.out_refs, rb, 4));
+  MISA_TRY(check_opt(u.n_live, 4, 4));
+  MISA_TRY(check_opt(u.status, 4, 4));
+  MISA_TRY(check_scratch(const_cast<void*>(u.ws), ws_bytes, need));
+  const Buffer table = {u.table, tb}, refs = {u.refs, rb}, x = {u.x, nb}, y = {u.y, nb};
+  const Buffer out_table = {u.out_table, tb}, out_refs = {u.out_refs, rb}, n_live = {u.n_live, 4};
+  const Buffer status = {u.status, 4}, ws = {need ? u.ws : nullptr, need};
+  MISA_TRY(check_apart({out_table, out_refs, n_live, status, ws},
+                       {unless(u.out_table, table), unless(u.out_refs, refs), x, y}));
+  for (int i = 0; pools && i < pools->n; ++i)
+    MISA_TRY(check_apart({{pools->base[i], (size_t)num_pages * pools->page_bytes[i]}},
+                         {table, refs, x, y, out_table, out_refs, n_live, status, ws}));
+  return MISA_OK;
 }
 
 int take_pools(void* const* pools, const int64_t* page_bytes, int npools, int num_pages,
@@ -92,6 +125,11 @@ int take_pools(void* const* pools, const int64_t* page_bytes, int npools, int nu
     out->base[i] = static_cast<unsigned char*>(pools[i]);
     out->page_bytes[i] = (uint32_t)page_bytes[i];
   }
+  Buffer all[MISA_MAX_POOLS];
+  for (int i = 0; i < npools; ++i) all[i] = {pools[i], (size_t)num_pages * page_bytes[i]};
+  std::sort(all, all + npools, [](const Buffer& x, const Buffer& y) { return x.p < y.p; });
+  for (int i = 1; i < npools; ++i)
+    if (overlap(all[i - 1], all[i])) return MISA_ERR_INVALID_ARG;
   return MISA_OK;
 }
 
@@ -135,21 +173,19 @@ static int paged_attention(const void* q, const void* k_cache, const void* v_cac
   MISA_TRY(check_dev(out, rows * Hq * d * 2, 16));
   MISA_TRY(check_opt(lse, rows * Hq * 4, 4));
   MISA_TRY(check_opt(device_status, 4, 4));
-  const size_t ob = rows * Hq * d * 2, lb = rows * Hq * 4;
-  MISA_TRY(check_out(q, out, ob));
-  MISA_TRY(check_apart(out, ob, k_cache, pool));
-  MISA_TRY(check_apart(out, ob, v_cache, pool));
-  if (lse) {
-    MISA_TRY(check_apart(lse, lb, out, ob));
-    MISA_TRY(check_apart(lse, lb, q, ob));
-    MISA_TRY(check_apart(lse, lb, k_cache, pool));
-    MISA_TRY(check_apart(lse, lb, v_cache, pool));
-  }
   PagedAttn p = {q,    k_cache, v_cache, page_table, pos, idx,       out,       lse,       dtype,
                  nseq, T,       Hq,      Hkv,        d,   num_pages, page_size, max_pages, topk,
                  scale, probe};
   if (probe && !paged_attn_tc(p)) return MISA_ERR_UNSUPPORTED;
-  MISA_TRY(check_scratch(ws, ws_bytes, paged_attn_ws_bytes(p)));
+  const size_t need = paged_attn_ws_bytes(p);
+  MISA_TRY(check_scratch(ws, ws_bytes, need));
+  const Buffer queries = {q, rows * Hq * d * 2}, result = {out, queries.bytes};
+  const Buffer sums = {lse, rows * Hq * 4}, scratch = {need ? ws : nullptr, need};
+  const Buffer status = {device_status, 4};
+  MISA_TRY(check_apart({result, sums, scratch, status},
+                       {{k_cache, pool}, {v_cache, pool}, {page_table, (size_t)nseq * max_pages * 4},
+                        {pos, rows * 4}, {idx, rows * topk * 4}, unless(out, queries)}));
+  if (q == out) MISA_TRY(check_apart({sums, scratch, status}, {queries}));
   return cuda_status(launch_paged_attn(p, ws, device_status, (cudaStream_t)stream));
 }
 
@@ -193,8 +229,9 @@ int misa_paged_append(const void* k_new, const void* v_new, const int32_t* pos,
   MISA_TRY(check_dev(page_table, (size_t)nseq * max_pages * 4, 4));
   MISA_TRY(check_dev(k_cache, pool, 16));
   MISA_TRY(check_dev(v_cache, pool, 16));
-  MISA_TRY(check_apart(k_cache, pool, v_cache, pool));
   MISA_TRY(check_opt(device_status, 4, 4));
+  MISA_TRY(check_apart({{k_cache, pool}, {v_cache, pool}, {device_status, 4}},
+                       {{page_table, (size_t)nseq * max_pages * 4}, {pos, rows * 4}}));
   return cuda_status(launch_paged_append(k_new, v_new, pos, page_table, nseq, T, Hkv * d * 2,
                                          num_pages, page_size, max_pages, k_cache, v_cache,
                                          device_status, (cudaStream_t)stream));
@@ -221,13 +258,14 @@ int misa_pages_resize(const int32_t* page_table, const int32_t* refs, const int3
   MISA_TRY(check_table(nseq, max_pages, num_pages));
   if (page_size < 1) return MISA_ERR_INVALID_ARG;
   if ((int64_t)max_pages * page_size > kMaxSpan) return MISA_ERR_UNSUPPORTED;
-  MISA_TRY(check_upkeep(MISA_OP_PAGES_RESIZE, page_table, refs, nseq, max_pages, num_pages, out_table,
-                        out_refs, ws, ws_bytes));
   MISA_TRY(check_dev(old_len, (size_t)nseq * 4, 4));
   MISA_TRY(check_dev(new_len, (size_t)nseq * 4, 4));
-  MISA_TRY(check_opt(device_status, 4, 4));
   PagePools pp;
   MISA_TRY(take_pools(pools, page_bytes, npools, num_pages, &pp));
+  MISA_TRY(check_upkeep(MISA_OP_PAGES_RESIZE,
+                        {page_table, refs, old_len, new_len, out_table, out_refs, nullptr,
+                         device_status, ws},
+                        nseq, max_pages, num_pages, ws_bytes, &pp));
   return cuda_status(launch_pages_resize(page_table, refs, old_len, new_len, nseq, max_pages,
                                          num_pages, page_size, pp, out_table, out_refs, ws,
                                          device_status, (cudaStream_t)stream));
@@ -238,10 +276,11 @@ int misa_pages_fork(const int32_t* page_table, const int32_t* refs, const int32_
                     int32_t* out_refs, int32_t* device_status, void* ws, size_t ws_bytes,
                     void* stream) {
   MISA_TRY(check_table(nseq, max_pages, num_pages));
-  MISA_TRY(check_upkeep(MISA_OP_PAGES_FORK, page_table, refs, nseq, max_pages, num_pages, out_table,
-                        out_refs, ws, ws_bytes));
   MISA_TRY(check_dev(parent, (size_t)nseq * 4, 4));
-  MISA_TRY(check_opt(device_status, 4, 4));
+  MISA_TRY(check_upkeep(MISA_OP_PAGES_FORK,
+                        {page_table, refs, parent, nullptr, out_table, out_refs, nullptr,
+                         device_status, ws},
+                        nseq, max_pages, num_pages, ws_bytes, nullptr));
   return cuda_status(launch_pages_fork(page_table, refs, parent, nseq, max_pages, num_pages,
                                        out_table, out_refs, ws, device_status,
                                        (cudaStream_t)stream));
@@ -252,12 +291,12 @@ int misa_pages_compact(const int32_t* page_table, const int32_t* refs, int nseq,
                        int32_t* out_table, int32_t* out_refs, int32_t* n_live,
                        int32_t* device_status, void* ws, size_t ws_bytes, void* stream) {
   MISA_TRY(check_table(nseq, max_pages, num_pages));
-  MISA_TRY(check_upkeep(MISA_OP_PAGES_COMPACT, page_table, refs, nseq, max_pages, num_pages, out_table,
-                        out_refs, ws, ws_bytes));
-  MISA_TRY(check_opt(n_live, 4, 4));
-  MISA_TRY(check_opt(device_status, 4, 4));
   PagePools pp;
   MISA_TRY(take_pools(pools, page_bytes, npools, num_pages, &pp));
+  MISA_TRY(check_upkeep(MISA_OP_PAGES_COMPACT,
+                        {page_table, refs, nullptr, nullptr, out_table, out_refs, n_live,
+                         device_status, ws},
+                        nseq, max_pages, num_pages, ws_bytes, &pp));
   return cuda_status(launch_pages_compact(page_table, refs, nseq, max_pages, num_pages, pp,
                                           out_table, out_refs, n_live, ws, device_status,
                                           (cudaStream_t)stream));
