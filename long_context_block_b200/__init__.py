@@ -84,7 +84,8 @@ def misa_sparse_attention(qi, w, ki, pos, B: int, h: int, topk: int, q, k_cache,
     over them.  qi, w, ki: the indexer's queries, head weights and keys (the step's included); q:
     the attention's queries; pos: the positions of both, -1 for padded rows, which append nothing,
     select nothing (idx -1) and get out 0.  ki is dense, [nseq, L, 128]: a caller that forks pages
-    reorders its rows too.  Returns (out, idx, heads)."""
+    reorders its rows too.  The indexer's workspace is one per device: calls on several streams must
+    not overlap.  Returns (out, idx, heads)."""
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new come together")
     if k_new is not None:

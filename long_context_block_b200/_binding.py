@@ -145,20 +145,40 @@ class _Workspace:
 
     Every call on a device uses this buffer, so (as the C ABI requires of one workspace)
     calls issued on different streams must not overlap on the GPU: synchronise the streams
-    between them, or call the C entry points with a workspace per stream."""
+    between them, or call the C entry points with a workspace per stream.  A buffer that a
+    captured graph uses is kept for good when a larger one takes its place; make a call of a
+    graph's sizes before its capture, so that the buffer is none of the graph's own memory."""
+
+    _HEADER = 256      # bytes, with the status word
 
     def __init__(self):
         self._buf = {}
+        self._captured = {}      # buffers that graphs hold, by device
         self._lock = threading.Lock()
 
     def get(self, nbytes: int, device) -> torch.Tensor:
         dev = torch.device(device)
+        capturing = torch.cuda.is_current_stream_capturing()
         with self._lock:
+            held = self._captured.setdefault(dev.index, [])
             b = self._buf.get(dev.index)
             if b is None or b.numel() < nbytes:
-                b = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+                old, b = b, torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+                if old is not None and not any(x is old for x in held):
+                    if capturing:
+                        held.append(old)
+                    else:       # a condition recorded there moves along
+                        b[:self._HEADER] = old[:self._HEADER]
                 self._buf[dev.index] = b
+            if capturing and not any(x is b for x in held):
+                held.append(b)
             return b
+
+    def words(self, dev: torch.device) -> list[torch.Tensor]:
+        """Buffers that may hold a condition: the present one and those of captured graphs."""
+        b = self.get(self._HEADER, dev)
+        with self._lock:
+            return [b] + [x for x in self._captured.get(dev.index, ()) if x is not b]
 
 
 _WS = _Workspace()
@@ -203,11 +223,11 @@ _STATUS = _Status()
 
 def misa_check_device_status(device=None) -> int:
     """Synchronise the current stream, read and clear the status words (the workspace's, then the
-    paged-cache calls'); raise if one is set.  Where both are, the second stays for the next call."""
+    paged-cache calls'); raise if one is set.  Where several are, the others stay for the next call."""
     dev = torch.device(device if device is not None else "cuda")
     if dev.index is None:      # the current device, whose buffers are kept under its number
         dev = torch.device("cuda", torch.cuda.current_device())
-    for word in (_WS.get(256, dev), _STATUS.find(dev.index)):
+    for word in (*_WS.words(dev), _STATUS.find(dev.index)):
         if word is not None:
             _check("misa_check_device_status",
                    int(_lib.misa_check_device_status(_ptr(word), _stream())))

@@ -36,3 +36,55 @@ def test_both_kinds_of_condition_are_reported(M, device):
     assert [status(M, device) for _ in range(2)] == [6, 0]
     out_of_pages(M)
     assert [status(M, device) for _ in range(2)] == [8, 0]
+
+
+def fresh_workspace(M, monkeypatch):
+    from long_context_block_b200 import _binding as b
+    monkeypatch.setattr(b, "_WS", b._Workspace())
+    return b._WS
+
+
+def call(M, L, pos, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randn((8, 1, 8, 128), generator=g, device="cuda").bfloat16()
+    k = torch.randn((8, L, 128), generator=g, device="cuda").bfloat16()
+    w = torch.randn((8, 1, 8), generator=g, device="cuda")
+    pos = torch.full((8, 1), pos, dtype=torch.int32, device="cuda")
+    return q, w, k, pos, lambda: M.misa_indexer(q, w, k, pos, 64, 3, 100)
+
+
+def test_a_condition_outlives_a_larger_workspace(M, monkeypatch):
+    ws = fresh_workspace(M, monkeypatch)
+    bad_position(M)
+    small = ws.get(0, "cuda:0").numel()
+    call(M, 120_000, 119_999)[-1]()
+    assert ws.get(0, "cuda:0").numel() > small
+    assert [status(M, 0) for _ in range(2)] == [6, 0]
+
+
+def test_a_graph_keeps_its_workspace(M, monkeypatch):
+    """A captured indexer step replayed after larger calls: its results stay, and so does memory
+    that was allocated in between."""
+    ws = fresh_workspace(M, monkeypatch)
+    q, w, k, pos, f = call(M, 30_000, 29_999)
+    want = [x.clone() for x in f()]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = f()
+    before = ws.get(0, "cuda:0")
+    call(M, 200_000, 199_999)[-1]()
+    assert ws.get(0, "cuda:0") is not before
+    size = before.numel()
+    del before
+    others = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for x in got:
+        x.fill_(0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert all(bool((x == 7).all()) for x in others)
+    assert status(M, 0) == 0
+    pos.fill_(30_000)                       # what a replay reports shows
+    g.replay()
+    assert [status(M, 0) for _ in range(2)] == [6, 0]
+    del g
