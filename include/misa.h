@@ -265,14 +265,16 @@ int misa_score_topk_noalloc(const uint16_t* q, const float* w, const uint16_t* k
  * q itself; otherwise what is written (out, lse, ws, device_status) must not overlap anything else.
  * Sums and softmax statistics are fp32; the weights p are rounded to dtype for their product with
  * v.  In fp16 those down to 2^-25 of their row's largest keep the type's precision, those below
- * 2^-36 of it count as 0 there.  A row whose largest score is beyond what they hold (2^30 / log2 e = 7e8 in magnitude, in
- * fp16 2^26 / log2 e = 4e7) is NaN.
- * A NaN or infinite key or value shows in the queries that see it, and in no other. (An infinite
+ * 2^-36 of it count as 0 there.  A row whose largest score is beyond what they hold (2^30 / log2 e =
+ * 7e8 in magnitude, in fp16 2^26 / log2 e = 4e7) is NaN.
+ * A NaN or infinite key or value shows in the queries that see it, and in no other.  (An infinite
  * value whose weight is 0, by a score of -inf or one that vanishes in fp32, may show as itself, as
  * NaN or not at all.)
  * Made for few queries per sequence (decode, drafts): 128 / (Hq / Hkv) queries share one
- * reading of the cache.  ws: misa_paged_attention_workspace_size(...) bytes (0 where few or short items
- * need none, and on invalid arguments; ws may then be NULL).
+ * reading of the cache.  How the work is split follows from max_pages * page_size, taken for the
+ * longest sequence; a table no wider than needed is quickest for short ones.
+ * ws: misa_paged_attention_workspace_size(...) bytes (0 where few or short items need none, and on
+ * invalid arguments; ws may then be NULL).
  */
 size_t misa_paged_attention_workspace_size(int nseq, int T, int Hq, int Hkv, int d,
                                            int page_size, int max_pages, int topk);

@@ -500,7 +500,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 }
 
 // CTAs that share an item: 0 for equal ranges.  The longest item there can be decides, as the
-// lengths are known on the device only.
+// lengths are known on the device only: one sequence of 777 tokens takes 6.2 us under a table of its
+// own width, 9.0 us under one for 131072 tokens.
 //   Time of a unit (32 KB) per CTA: 1.48 us where all 296 CTAs stream (the memory's rate), 0.9 us
 //   where few do (latency).  Shared items pay full waves of CTAs and a last, partial one; equal
 //   ranges pay the average and about 3 us for the join: 64 items of 2048 selected tokens 17.7
