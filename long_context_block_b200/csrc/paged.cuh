@@ -142,10 +142,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 //
 // A weight's exponent is s scale2 - m in one rounding, m the largest score's product, rounded too.
 // So a row's largest weight is off by a factor 2^x, x up to half a step of m: 2^-4 where m is 2^20
-// (log2 domain), 32 where it is 2^30, which bf16 and fp32 take.  fp16 ends at 2^16, so there m is
-// rounded upward: the weights get smaller at such scores, down to 2^-8 times where m is 2^26, but
-// none overflows.  Beyond that the largest weight could come out as 0 or infinite, so a row's sum
-// becomes NaN, and with it its output.
+// (log2 domain), 32 where it is 2^30.  m is rounded upward where that counts (beyond 2^20; in fp16,
+// which ends at 2^16, always): the weights get smaller at such scores, but none overflows.  They
+// still do at 2^26 in fp16 and 2^30 in bf16; beyond, the largest weight may vanish, so a row whose
+// largest score is beyond is NaN (finish).  Scores as far below the row's largest are weights of 0.
 template <typename E>
 struct Weights {
   static constexpr bool kFp16 = !IsBf16<E>::value;
@@ -154,11 +154,13 @@ struct Weights {
   static constexpr float kLargest = kFp16 ? 67108864.f : 1073741824.f;
   // What a row's exponents are taken from (log2 domain): its largest score `top`, in fp16 less `up`.
   static __device__ __forceinline__ float reference(float top, float scale2, float up) {
-    return kFp16 ? __fadd_ru(__fmul_ru(top, scale2), -up) : top * scale2;
+    const float above = __fmul_ru(top, scale2);
+    if constexpr (kFp16) return __fadd_ru(above, -up);
+    return fabsf(above) > 1048576.f ? above : top * scale2;
   }
-  // the sum l of a row whose reference has moved to m
-  static __device__ __forceinline__ float checked(float l, float m) {
-    return fabsf(m) > kLargest && m != -INFINITY ? NAN : l;   // -inf: no score yet
+  // Whether a row of reference m in the end is past that (-inf: no score).
+  static __device__ __forceinline__ bool beyond(float m) {
+    return fabsf(m) > kLargest && m != -INFINITY;
   }
 };
 

@@ -312,7 +312,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Entry<16 * MT, S
       for (int r = 0; r < 2 * MT; ++r) {
         const float f = mx[r] == m[r] ? 1.f : exp2_approx(m[r] - mx[r]);
         m[r] = mx[r];
-        l[r] = Weights<E>::checked(l[r] * f, m[r]);
+        l[r] *= f;
 #pragma unroll
         for (int x = 0; x < DN; ++x) {
           o[r >> 1][x][(r & 1) * 2] *= f;

@@ -117,6 +117,7 @@ __device__ __forceinline__ void finish(const AttnArgs& a, int n, int rr, int hk,
                                        const float4& acc, float mm, float ll) {
   const int t = rr / a.G, g = rr - t * a.G;
   const int64_t head = ((int64_t)n * a.T + t) * a.Hq + hk * a.G + g;
+  if (Weights<E>::beyond(mm)) ll = NAN;
   const float inv = ll == 0.f ? 0.f : 1.f / ll;
   uint2 y;
   y.x = pack2<E>(acc.x * inv, acc.y * inv);

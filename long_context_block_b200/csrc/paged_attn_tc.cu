@@ -322,11 +322,10 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
           const float top =
               Weights<E>::reference(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.scale2,
                                     Weights<E>::kTop - kSlack<E>);
-          const float most = Weights<E>::kFp16 ? __fadd_rd(m, kSlack<E>) : m + kSlack<E>;
-          if (__any_sync(0xffffffffu, top > most)) {   // the maximum moves, O with it
+          if (__any_sync(0xffffffffu, top > __fadd_rd(m, kSlack<E>))) {   // the maximum moves, O with it
             const float up = fmaxf(m, top), f = up == m ? 1.f : exp2_approx(m - up);
             m = up;
-            l = Weights<E>::checked(l * f, m);
+            l *= f;
             if (behind) {
               if (!(ok = warp_wait(odone, gi - 1))) break;
               behind = false;
@@ -380,6 +379,7 @@ paged_attn_tc_kernel(const __grid_constant__ AttnArgs a) {
           f[k] = x[k].x == m ? 1.f : exp2_approx(x[k].x - m);
           l += x[k].y * f[k];
         }
+        if (whole && Weights<E>::beyond(m)) l = f[0] = f[1] = NAN;
       }
       if (warp_live) {
         const int64_t head = ((int64_t)en.n * a.T + t) * a.Hq + sg.hk * a.G + (rr - t * a.G);

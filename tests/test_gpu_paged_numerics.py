@@ -8,7 +8,6 @@ import pytest
 import torch
 
 import oracle.paged_oracle as po
-
 from tests.test_gpu_paged import M, Case, f64, form   # noqa: F401 (M is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -77,6 +76,48 @@ def test_scores_beyond_the_largest_show(M, name, sign, dtype):
     out, lse = c.run(M)
     assert M.misa_check_device_status(out.device) == 0
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("where", ["first", "last", "spread"])
+@pytest.mark.parametrize("name", list(EVERY_FORM))
+def test_scores_far_below_the_largest_weigh_nothing(M, name, where, dtype):
+    """Tokens whose scores are -1.8e9, beyond what a row's largest may be: the outputs are those of
+    the other tokens (Case.check's bound over them), wherever in the sequence they stand."""
+    c = Case(**EVERY_FORM[name], dtype=dtype, poison=False, seed=6, scale=2.0)
+    assert form(M, c) == name.split("_")[0]
+    d = c.q.shape[-1]
+    c.q[..., 0] = 30000
+    c.k.mul_(0.05)
+    c.k[..., 0] = 0
+    low = [set(range(min(x, 70))) if where == "first" else set(range(x - 3, x)) if where == "last"
+           else set(range(0, x, 3)) for x in c.lens]
+    for n, tokens in enumerate(low):
+        for s in tokens:
+            c.k[c.table[n, s // c.ps], s % c.ps, :, 0] = -30000
+    out, lse = c.run(M)
+    assert M.misa_check_device_status(out.device) == 0
+    q, k, v, got, lse = f64(c.q), f64(c.k), f64(c.v), f64(out), f64(lse)
+    u, e, rows = torch.finfo(c.q.dtype).eps / 2, 2.0 ** -23, 0
+    q0 = q.copy()
+    q0[..., 0] = 0                    # adds nothing to the other tokens' scores, nor their errors
+    for n in (0, 1, len(c.lens) - 1):
+        for t in {0, c.T - 1}:
+            seen = [s for s in c.seen(n, t) if s not in low[n]]
+            if not seen:
+                assert not c.seen(n, t) or np.isnan(got[n, t]).all()
+                continue
+            rows += 1
+            ref, rl, mean, mag = po.attention_row(q0[n, t], k, v, c.table[n], c.ps, seen, c.scale)
+            S, dz = len(seen), (d + 8) * e * mag
+            w = u + 2 * dz + 2.0 ** -22 + 2 * (S + 16) * e
+            bound = u * 1.02 * np.abs(ref) + w[:, None] * mean + torch.finfo(c.q.dtype).tiny * u
+            if dtype == "fp16":       # small weights: see below
+                bound += S * 2.0 ** -36 * np.abs(v).max()
+            assert np.all(np.abs(got[n, t] - ref) <= bound), (n, t)
+            assert np.all(np.abs(lse[n, t] - rl)
+                          <= dz + 2.0 ** -22 + (S + 16) * e + 4 * e * np.abs(rl)), (n, t)
+    assert rows > 0
 
 
 @pytest.mark.parametrize("name", ["cluster", "ranges", "tc_one_tile", "tc_whole"])
