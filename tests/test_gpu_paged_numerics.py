@@ -288,3 +288,14 @@ def test_one_infinite_value_does_not_hold_up_a_long_call(M):
     assert M.misa_check_device_status("cuda") == 0
     ref[:, 1:, :, 11] = float("inf")
     assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("kw", [dict(Hq=8, Hkv=2), dict(Hq=40, Hkv=1, d=64, dtype="fp16")])
+def test_a_prompt_over_its_selected_tokens(M, kw):
+    """Thousands of queries of one sequence, each with tokens of its own and the first ones with
+    fewer than the list holds."""
+    c = Case([3000], T=3000, topk=200, ps=64, poison=False, **kw)
+    out, lse = c.run(M)
+    assert M.misa_check_device_status(out.device) == 0
+    c.check(out, lse, rows={(0, t) for t in (0, 1, 63, 199, 200, 1511, 2048, 2998, 2999)})
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
