@@ -141,11 +141,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // keep fp16's precision, and those below 2^-36 of it vanish (2^-14 and 2^-25 with the largest at 1).
 //
 // A weight's exponent is s scale2 - m in one rounding, m the largest score's product, rounded too.
-// So a row's largest weight is off by a factor 2^x, x up to half a step of m: 2^-4 where m is 2^20
-// (log2 domain), 32 where it is 2^30.  m is rounded upward where that counts (beyond 2^20; in fp16,
-// which ends at 2^16, always): the weights get smaller at such scores, but none overflows.  They
-// still do at 2^26 in fp16 and 2^30 in bf16; beyond, the largest weight may vanish, so a row whose
-// largest score is beyond is NaN (finish).  Scores as far below the row's largest are weights of 0.
+// So a row's largest weight is off by a factor 2^x, x up to half a step of m (2^-4 where m is 2^20,
+// log2 domain).  m is rounded upward where that counts (beyond 2^20; in fp16, which ends at 2^16,
+// always): the weights then get smaller, by up to 2^-8 where m is 2^26 and 2^-64 where it is 2^30,
+// but none overflows.  That is as much as fp16 and bf16 take.  Beyond, the largest weight may vanish,
+// so a row whose largest score is beyond is NaN (finish); scores so far below a row's largest weigh
+// nothing.
 template <typename E>
 struct Weights {
   static constexpr bool kFp16 = !IsBf16<E>::value;
